@@ -1,7 +1,6 @@
 // Host side of libttc05: the C ABI declared in include/gemm_f16.h.
 //
-// Argument validation, per-device context (SM count, status word), TMA
-// tensor-map encoding, the choice between the tile kernels and the small-M
+// Argument validation, the choice between the tile kernels and the small-M
 // kernel, the small-M workspace cache and the status/self-test entry points.
 // The computation itself is the fused GEMM + ReLU of "Writing high-performance
 // kernels in TileLang" (atlascloud.ai blog), section "Escribamos un GEMM".
@@ -9,7 +8,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <cstdlib>
 #include <mutex>
 #include <vector>
 
@@ -18,24 +16,9 @@
 #include "sm100.cuh"
 
 namespace ttc {
-
-// One status word per device (first device-side error wins; 0 = none).
-__device__ int g_device_status;
-
 namespace {
 
-constexpr uint64_t kDefaultTimeoutNs = 1000ull * 1000ull * 1000ull;  // 1 s per wait
-constexpr int kMaxDevices = 64;
-
-struct DeviceEntry {
-  bool ready = false;
-  bool supported = false;
-  int sm_count = 0;
-  int* status = nullptr;
-};
-
 std::mutex g_mutex;
-DeviceEntry g_devices[kMaxDevices];
 
 struct Workspace {
   int device;
@@ -45,117 +28,10 @@ struct Workspace {
 };
 std::vector<Workspace> g_workspaces;
 
-// ------------------------------------------------------ driver entry points ---
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-typedef CUresult (*AddressRangeFn)(CUdeviceptr*, size_t*, CUdeviceptr);
-typedef CUresult (*PointerAttrsFn)(unsigned int, CUpointer_attribute*, void**, CUdeviceptr);
-
-EncodeTiledFn g_encode = nullptr;
-AddressRangeFn g_addr_range = nullptr;
-PointerAttrsFn g_ptr_attrs = nullptr;
-std::once_flag g_entry_once;
-
-void load_entry_points() {
-  std::call_once(g_entry_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-    fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_addr_range = reinterpret_cast<AddressRangeFn>(fn);
-    fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_ptr_attrs = reinterpret_cast<PointerAttrsFn>(fn);
-  });
-}
-
-// ------------------------------------------------------------ device state ---
-int get_device(DeviceCtx* ctx) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_LAUNCH;
-  if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED_DEVICE;
-  std::lock_guard<std::mutex> lock(g_mutex);
-  DeviceEntry& e = g_devices[dev];
-  if (!e.ready) {
-    int major = 0, minor = 0, sms = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return GEMM_ERR_LAUNCH;
-    e.supported = (major == 10 && minor == 0);
-    e.sm_count = sms;
-    if (e.supported) {
-      // The symbol's device address for this device (host code cannot use the
-      // symbol itself as a pointer).
-      void* p = nullptr;
-      if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return GEMM_ERR_LAUNCH;
-      e.status = static_cast<int*>(p);
-    }
-    e.ready = true;
-  }
-  if (!e.supported) return GEMM_ERR_UNSUPPORTED_DEVICE;
-  ctx->device = dev;
-  ctx->sm_count = e.sm_count;
-  ctx->status = e.status;
-  ctx->timeout_ns = kDefaultTimeoutNs;
-  return GEMM_OK;
-}
-
-// Device memory of the current device (or managed memory) only.
-bool is_device_pointer(const void* p, int device) {
-  cudaPointerAttributes attr;
-  if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
-    cudaGetLastError();  // clear the sticky-free error state of this query
-    return false;
-  }
-  if (attr.type == cudaMemoryTypeManaged) return true;
-  return attr.type == cudaMemoryTypeDevice && attr.device == device;
-}
-
-// The bytes [p, p + (rows-1)*ld*2 + cols*2) lie in one allocation.
-bool extent_in_allocation(const void* p, int64_t rows, int64_t cols, int64_t ld) {
-  if (g_addr_range == nullptr) return true;  // cannot check; TMA bounds still apply
-  CUdeviceptr base = 0;
-  size_t size = 0;
-  if (g_addr_range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return false;
-  const uint64_t start = reinterpret_cast<uint64_t>(p);
-  const uint64_t span = (static_cast<uint64_t>(rows - 1) * static_cast<uint64_t>(ld) +
-                         static_cast<uint64_t>(cols)) * 2u;
-  return start >= base && start - base + span <= size;
-}
-
-// One driver query for memory type, owning device and allocation range.
-// Returns -1 when the query itself is unavailable (caller falls back).
-int query_pointer(const void* p, int device, int64_t rows, int64_t cols, int64_t ld) {
-  if (g_ptr_attrs == nullptr) return -1;
-  unsigned int mem_type = 0;
-  int ordinal = -1;
-  unsigned int managed = 0;
-  CUdeviceptr base = 0;
-  size_t size = 0;
-  CUpointer_attribute attrs[5] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE,
-                                  CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
-                                  CU_POINTER_ATTRIBUTE_IS_MANAGED,
-                                  CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
-                                  CU_POINTER_ATTRIBUTE_RANGE_SIZE};
-  void* data[5] = {&mem_type, &ordinal, &managed, &base, &size};
-  if (g_ptr_attrs(5, attrs, data, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return 0;
-  const bool on_device = (mem_type == CU_MEMORYTYPE_DEVICE && ordinal == device) || managed != 0;
-  if (!on_device || size == 0) return 0;
-  const uint64_t start = reinterpret_cast<uint64_t>(p);
-  const uint64_t span = (static_cast<uint64_t>(rows - 1) * static_cast<uint64_t>(ld) +
-                         static_cast<uint64_t>(cols)) * 2u;
-  return (start >= base && start - base + span <= size) ? 1 : 0;
+// Bytes from the first to the last element of an fp16 matrix.
+uint64_t fp16_span(int64_t rows, int64_t cols, int64_t ld) {
+  return (static_cast<uint64_t>(rows - 1) * static_cast<uint64_t>(ld) +
+          static_cast<uint64_t>(cols)) * 2u;
 }
 
 int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int device) {
@@ -163,13 +39,7 @@ int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int devi
   if (ld < cols || ld < 1) return GEMM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0 || (ld & 7) != 0) return GEMM_ERR_ALIGNMENT;
   if (static_cast<uint64_t>(ld) * 2u >= (1ull << 40)) return GEMM_ERR_INVALID_ARG;
-  const int q = query_pointer(p, device, rows, cols, ld);
-  if (q == 0) return GEMM_ERR_INVALID_ARG;
-  if (q < 0) {
-    if (!is_device_pointer(p, device)) return GEMM_ERR_INVALID_ARG;
-    if (!extent_in_allocation(p, rows, cols, ld)) return GEMM_ERR_INVALID_ARG;
-  }
-  return GEMM_OK;
+  return check_device_range(p, device, fp16_span(rows, cols, ld));
 }
 
 int get_workspace(const DeviceCtx& d, cudaStream_t stream, void** ptr, size_t* bytes) {
@@ -287,38 +157,6 @@ int read_and_clear_status(const DeviceCtx& d, cudaStream_t stream, int* out) {
 }
 
 }  // namespace
-
-int encode_tmap_f16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                       uint64_t ld, uint32_t box_inner, uint32_t box_outer) {
-  load_entry_points();
-  if (g_encode == nullptr) return GEMM_ERR_LAUNCH;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {ld * 2u};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estrides[2] = {1, 1};
-  // (L2 promotion none / 128 B / 256 B measured alike on the pair kernels:
-  // the same DRAM bytes and time)
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
-                              dims, strides, box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_ARG;
-}
-
-bool pdl_enabled() {
-  static const bool on = [] {
-    const char* s = std::getenv("TTC_PDL");
-    return !(s != nullptr && s[0] == '0');
-  }();
-  return on;
-}
-
-int pdl_attribute(cudaLaunchAttribute* attr) {
-  if (!pdl_enabled()) return 0;
-  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr->val.programmaticStreamSerializationAllowed = 1;
-  return 1;
-}
 
 int launch_bias_act_fill(const GemmProblem& p) {
   const int64_t total = p.M * p.N;
@@ -651,9 +489,8 @@ int gemm_activation_f32(const void* x, void* y, int64_t n, int activation,
   int rc = get_device(&d);
   if (rc != GEMM_OK) return rc;
   load_entry_points();
-  // n floats = n / 2 rows... checked as one row of 2n fp16-sized elements
-  if (query_pointer(x, d.device, 1, 2 * n, 2 * n) != 1 ||
-      query_pointer(y, d.device, 1, 2 * n, 2 * n) != 1)
+  const uint64_t span = 4u * static_cast<uint64_t>(n);
+  if (query_pointer(x, d.device, span) != 1 || query_pointer(y, d.device, span) != 1)
     return GEMM_ERR_INVALID_ARG;
   int64_t blocks = (n + 255) / 256;
   if (blocks > 4096) blocks = 4096;
@@ -724,8 +561,8 @@ int gemm_read_probe(const void* src, int64_t n_bytes, void* sink, gemm_stream_t 
   if (rc != GEMM_OK) return rc;
   load_entry_points();
   // the sink: one 4-byte word; the source: n_bytes as one row
-  if (query_pointer(sink, d.device, 1, 2, 2) != 1) return GEMM_ERR_INVALID_ARG;
-  if (n_bytes > 0 && query_pointer(src, d.device, 1, n_bytes / 2, n_bytes / 2) != 1)
+  if (query_pointer(sink, d.device, 4) != 1) return GEMM_ERR_INVALID_ARG;
+  if (n_bytes > 0 && query_pointer(src, d.device, static_cast<uint64_t>(n_bytes)) != 1)
     return GEMM_ERR_INVALID_ARG;
   if (cudaMemsetAsync(sink, 0, sizeof(unsigned), stream) != cudaSuccess) return GEMM_ERR_LAUNCH;
   if (n_bytes == 0) return GEMM_OK;

@@ -65,6 +65,19 @@ struct DeviceCtx {
   uint64_t timeout_ns;  // limit for every device-side wait
 };
 
+// The current device's context (host_common.cu).  Returns 0 or a GEMM_ERR_* code.
+int get_device(DeviceCtx* ctx);
+
+// Resolves the driver entry points the checks and tensor maps use (once).
+void load_entry_points();
+
+// One driver query for memory type, owning device and allocation range: 1 if
+// [p, p + span) is memory of `device` (or managed), 0 if not, -1 when the
+// query is unavailable.  check_device_range falls back to the runtime's
+// queries then and returns 0 or GEMM_ERR_INVALID_ARG.
+int query_pointer(const void* p, int device, uint64_t span);
+int check_device_range(const void* p, int device, uint64_t span);
+
 // Whether kernels are launched with programmatic stream serialisation, so
 // their set-up overlaps the previous kernel of the stream (TTC_PDL=0 turns it
 // off for comparisons).
@@ -80,6 +93,11 @@ int pdl_attribute(cudaLaunchAttribute* attr);
 // Returns 0 or a GEMM_ERR_* code.
 int encode_tmap_f16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                        uint64_t ld, uint32_t box_inner, uint32_t box_outer);
+
+// The same for a matrix of bytes: boxes of 128 bytes by box_outer rows, `ld`
+// in bytes (a multiple of 16).
+int encode_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                      uint64_t ld, uint32_t box_outer);
 
 // Large-shape path: persistent warp-specialised tcgen05 kernel, one SM per
 // 128 x block_n tile (GEMM_PATH_TILE), or a pair of SMs per 256 x 256
