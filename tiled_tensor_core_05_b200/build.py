@@ -1,11 +1,12 @@
-"""Build ``libttc05.so`` (the CUDA kernels and the C ABI) in-tree with nvcc.
+"""Build ``libttc05.so`` (the fp16 GEMM kernels and their C ABI) and
+``libttcmx.so`` (the microscaled operators) in-tree with nvcc.
 
     python -m tiled_tensor_core_05_b200.build [--force] [--verbose] [--ptxas-info]
 
 Every translation unit is compiled for sm_100a only
 (``-gencode arch=compute_100a,code=sm_100a``) with ``-lineinfo``, in
-parallel, then linked into a shared library next to this file.  The CUDA
-runtime is linked statically, so the library needs only the driver at run
+parallel, then linked into the shared libraries next to this file.  The CUDA
+runtime is linked statically, so the libraries need only the driver at run
 time.
 """
 from __future__ import annotations
@@ -23,9 +24,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libttc05.so")
-SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu",
-           "host_common.cu"]
-HEADERS = ["sm100.cuh", "internal.h", "skinny_common.cuh"]
+MX_LIB = os.path.join(PKG, "libttcmx.so")
+COMMON = ["host_common.cu"]  # linked into both libraries
+SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu"]
+MX_SOURCES = ["mx_api.cu", "mx_rows.cu", "mx_gemm_split.cu"]
+HEADERS = ["sm100.cuh", "internal.h", "skinny_common.cuh", "mx_internal.h", "mx_common.cuh",
+           "mx_umma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -41,16 +45,16 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "gemm_f16.h"))
+    files = [os.path.join(CSRC, s) for s in COMMON + SOURCES + MX_SOURCES + HEADERS]
+    files += [os.path.join(INCLUDE, h) for h in ("gemm_f16.h", "gemm_mx.h")]
     files.append(os.path.abspath(__file__))
     return files
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MX_LIB):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MX_LIB))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -73,13 +77,20 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if not force and not ptxas_info and not needs_build():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, ptxas_info, verbose), SOURCES))
-    tmp = LIB + f".tmp{os.getpid()}"
-    # only the extern "C" API (gemm_*) is exported
-    vs = os.path.join(BUILD_DIR, "exports.map")
+    sources = COMMON + SOURCES + MX_SOURCES
+    with cf.ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        objs = dict(zip(sources, ex.map(lambda s: _compile(s, ptxas_info, verbose), sources)))
+    # only the extern "C" API is exported: gemm_* of libttc05, mx_* of libttcmx
+    _link(MX_LIB, [objs[s] for s in COMMON + MX_SOURCES], "mx_*", verbose)
+    _link(LIB, [objs[s] for s in COMMON + SOURCES], "gemm_*", verbose)
+    return LIB
+
+
+def _link(lib: str, objs: list, exports: str, verbose: bool) -> None:
+    tmp = lib + f".tmp{os.getpid()}"
+    vs = os.path.join(BUILD_DIR, os.path.basename(lib) + ".map")
     with open(vs, "w") as f:
-        f.write("{ global: gemm_*; local: *; };\n")
+        f.write("{ global: %s; local: *; };\n" % exports)
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + [
         "-Xlinker", f"--version-script={vs}"]
     if verbose:
@@ -87,8 +98,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, lib)
 
 
 def main(argv=None):

@@ -1,0 +1,386 @@
+// C = act(A B^T + bias) for MX operands, small and middling shapes: swap-AB
+// tiles with K split over a cluster.
+//
+// A tile is 128 rows of B (columns of C, the MMA's M) by BN rows of A (the
+// MMA's N: 16 to 128), so a single token wastes none of the weight's
+// bandwidth.  The K range of a tile is split over the CTAs of a cluster; each
+// accumulates its part in TMEM, puts it in its own shared memory, and the
+// CTAs then add all parts in rank order through distributed shared memory,
+// each for its share of the tile.  Nothing is kept in device memory between
+// or during calls (no workspace, no counters), and the order of the sums is
+// fixed by the shape.
+//
+//   warp 0   TMA producer: elements by tensor maps into 128-byte-swizzled
+//            shared memory, scale tiles by plain bulk copies
+//   warp 1   TMEM allocation; scale tiles to TMEM (tcgen05.cp) and the
+//            block-scaled tcgen05.mma
+//   warps 2-5  accumulator -> shared memory; then all warps: sum, bias,
+//            activation, store
+#include <atomic>
+
+#include "mx_internal.h"
+#include "mx_umma.cuh"
+
+namespace ttc {
+namespace mx {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kTileN = 128;  // columns of C per tile
+
+template <int FMT, int BN>
+struct SplitCfg {
+  static constexpr int kStages = BN == 64 ? 4 : 3;
+  static constexpr int kWBytes = kTileN * kRowBytes;
+  static constexpr int kXBytes = BN * kRowBytes;
+  static constexpr int kSfBytes = Kind<FMT>::kSfTiles * kTileBytes;
+  static constexpr int kStageBytes = kWBytes + kXBytes + 2 * kSfBytes;
+  static constexpr int kPartBytes = BN * kTileN * 4;  // fp32 partial tile, over the ring
+  static constexpr int kRing = kStages * kStageBytes > kPartBytes ? kStages * kStageBytes : kPartBytes;
+  static constexpr int kSmemBytes = 1024 + kRing + (2 * kStages + 2) * 8 + 16;
+  // accumulator, then one set of scales per stage: a stage's columns are
+  // written again only after the MMAs that read them have completed
+  static constexpr int kSfBase = BN < 32 ? 32 : BN;
+  static constexpr int kCols = kSfBase + kStages * 2 * Kind<FMT>::kSfCols;
+  static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+  static_assert(kCols <= 256, "TMEM columns");
+  static_assert(kSmemBytes <= kMaxDynamicSmem, "shared memory budget");
+};
+
+struct SplitArgs {
+  const uint8_t *SB, *SA;
+  const uint16_t* bias;
+  uint16_t* C;
+  int64_t ldc;
+  int M, N;
+  int row_bytes;  // bytes of a row of elements
+  int tiles;      // scale tiles along K
+  int stages;     // ring stages along K
+  int tiles_m;
+  int dtype, act;
+  int* status;
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+
+// Eight columns of a row of C from their fp32 sums: bias, activation, one
+// rounding, stored as 16 bytes or, across the edge, one by one.
+template <class T>
+__device__ __forceinline__ void store_row8(const SplitArgs& a, int m, int n, const float (&v)[8]) {
+  const int count = min(8, a.N - n);
+  uint4 bias = make_uint4(0, 0, 0, 0);
+  if (a.bias != nullptr) bias = load8(a.bias + n, count);
+  float b[8], y[8];
+  unpack8<T>(bias, b);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 r = finish2(make_float2(v[i], v[i + 1]), make_float2(b[i], b[i + 1]), a.act);
+    y[i] = r.x;
+    y[i + 1] = r.y;
+  }
+  store8(a.C + static_cast<int64_t>(m) * a.ldc + n, pack8<T>(y), count);
+}
+
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kThreads)
+    split_gemm_kernel(const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmA, const SplitArgs a) {
+  using Cfg = SplitCfg<FMT, BN>;
+  constexpr int kStages = Cfg::kStages;
+  constexpr int kSfTiles = Kind<FMT>::kSfTiles;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* smW = smem;
+  uint8_t* smX = smW + kStages * Cfg::kWBytes;
+  uint8_t* smS = smX + kStages * Cfg::kXBytes;  // per stage: scales of B, scales of A
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kRing);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* drain = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int splits = static_cast<int>(cluster_size());
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tile = static_cast<int>(blockIdx.x) / splits;
+  const int mt = tile % a.tiles_m, nt = tile / a.tiles_m;
+  const int m0 = mt * BN, n0 = nt * kTileN;
+  const int rows = min(BN, a.M - m0);
+  const int s_begin = static_cast<int>(static_cast<int64_t>(a.stages) * rank / splits);
+  const int s_end = static_cast<int>(static_cast<int64_t>(a.stages) * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmA);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, Cfg::kTmemCols);
+    tmem_relinquish_alloc_permit();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_trigger();
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, parity = 0;
+      bool ok = true;
+      for (int s = s_begin; s < s_end; ++s) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        // the last stage may have one scale tile of two
+        const int kt = s * kSfTiles;
+        const uint32_t sf = static_cast<uint32_t>(min(kSfTiles, a.tiles - kt)) * kTileBytes;
+        mbar_arrive_expect_tx(&full[stage], Cfg::kWBytes + Cfg::kXBytes + 2 * sf);
+        tma_load_2d(&tmB, &full[stage], smW + stage * Cfg::kWBytes, s * kRowBytes, n0);
+        tma_load_2d(&tmA, &full[stage], smX + stage * Cfg::kXBytes, s * kRowBytes, m0);
+        uint8_t* sfw = smS + stage * 2 * Cfg::kSfBytes;
+        bulk_load(sfw, a.SB + (static_cast<int64_t>(nt) * a.tiles + kt) * kTileBytes, sf,
+                  &full[stage]);
+        bulk_load(sfw + Cfg::kSfBytes,
+                  a.SA + (static_cast<int64_t>(m0 / kTileRows) * a.tiles + kt) * kTileBytes, sf,
+                  &full[stage]);
+        armed |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleProducer << 4) | 1);
+        // let every load already issued land before shared memory is released
+        for (int s = 0; s < kStages; ++s)
+          if (armed & (1u << s)) (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int s = s_begin; s < s_end; ++s) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, a.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t w_addr = smem_u32(smW + stage * Cfg::kWBytes);
+        const uint32_t x_addr = smem_u32(smX + stage * Cfg::kXBytes);
+        const uint32_t s_addr = smem_u32(smS + stage * 2 * Cfg::kSfBytes);
+        const uint32_t sfw = tmem + Cfg::kSfBase + stage * 2 * Kind<FMT>::kSfCols;
+        const uint32_t sfx = sfw + Kind<FMT>::kSfCols;
+        const int have = min(kSfTiles, a.tiles - s * kSfTiles);
+#pragma unroll
+        for (int t = 0; t < kSfTiles; ++t) {
+          if (t >= have) break;
+          copy_scales<1>(sfw + 4 * t, scale_desc(s_addr + t * kTileBytes));
+          copy_scales<1>(sfx + 4 * t, scale_desc(s_addr + Cfg::kSfBytes + t * kTileBytes));
+        }
+        // the last stage: only the MMAs that reach into the row
+        const int left = a.row_bytes - s * kRowBytes;
+#pragma unroll
+        for (int k = 0; k < kMmasPerStage; ++k) {
+          if (k * kMmaBytes >= left) break;
+          const int t = FMT == MX_FP8 ? 0 : k / 2;
+          mx_mma<FMT, 1>(tmem, smem_desc_sw128(w_addr + k * kMmaBytes, 16, 1024),
+                         smem_desc_sw128(x_addr + k * kMmaBytes, 16, 1024),
+                         mx_idesc<FMT>(kTileN, BN, k), sfw + 4 * t, sfx + 4 * t,
+                         (s != s_begin || k != 0) ? 1u : 0u);
+        }
+        umma_commit(&empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok) {
+        umma_commit(acc_full);
+      } else {
+        raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleMma << 4) | 1);
+        umma_commit(drain);
+        (void)mbar_wait(drain, 0, nullptr, a.timeout_ns);
+      }
+    }
+  } else {
+    int ok = 1;
+    if (lane == 0) ok = mbar_wait(acc_full, 0, abort_flag, a.timeout_ns) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok) {
+      // all loads have landed and all MMAs have read them: the ring is free
+      tc_fence_after_sync();
+      const int q = warp & 3;
+      float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        if (c >= rows) break;
+        uint32_t v[32];
+        tmem_load_32x32b_x32(t_row + c, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < rows) part[(c + i) * kTileN] = __uint_as_float(v[i]);
+      }
+    } else if (lane == 0) {
+      raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 1);
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  if (splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+
+  // items: (row, 8 columns), dealt out over the threads of the whole cluster
+  const uint32_t part = smem_u32(smem);
+  if (*abort_flag == 0) {
+    for (int it = rank * kThreads + threadIdx.x; it < rows * (kTileN / 8); it += splits * kThreads) {
+      const int m = it >> 4, n = n0 + (it & 15) * 8;
+      if (n >= a.N) continue;
+      const uint32_t at = part + static_cast<uint32_t>(m * kTileN + (it & 15) * 8) * 4;
+      float v[8] = {};
+      for (int s = 0; s < splits; ++s) {
+        const uint32_t src = map_to_cta(at, static_cast<uint32_t>(s));
+        const float4 x = ld_cluster_f4(src), y = ld_cluster_f4(src + 16);
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+      }
+      if (a.dtype == MX_F16)
+        store_row8<__half>(a, m0 + m, n, v);
+      else
+        store_row8<__nv_bfloat16>(a, m0 + m, n, v);
+    }
+  }
+  __syncwarp();
+  // no CTA leaves while another may still read its part
+  if (splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+template <int FMT, int BN>
+int launch(const MxGemmProblem& p, const DeviceCtx& d) {
+  using Cfg = SplitCfg<FMT, BN>;
+  static std::atomic<uint64_t> attr_done{0};
+  auto kern = split_gemm_kernel<FMT, BN>;
+  const uint64_t bit = 1ull << (d.device & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg::kSmemBytes) != cudaSuccess)
+      return GEMM_ERR_LAUNCH;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t row_bytes = mx_row_bytes(p.K, FMT);
+  CUtensorMap tB, tA;
+  int rc = encode_tmap_u8_2d(&tB, p.B, row_bytes, p.N, p.ldb, kTileN);
+  if (rc == 0) rc = encode_tmap_u8_2d(&tA, p.A, row_bytes, p.M, p.lda, BN);
+  if (rc != 0) return rc;
+  const int64_t stages = (row_bytes + kRowBytes - 1) / kRowBytes;
+  const int64_t tiles_m = (p.M + BN - 1) / BN;
+  const int64_t tiles = tiles_m * ((p.N + kTileN - 1) / kTileN);
+  const int resident = d.sm_count * (kMaxDynamicSmem / Cfg::kSmemBytes);
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= resident && stages >= splits * 4) splits *= 2;
+  if (tiles * splits > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+  const SplitArgs a{static_cast<const uint8_t*>(p.SB),
+                    static_cast<const uint8_t*>(p.SA),
+                    static_cast<const uint16_t*>(p.bias),
+                    static_cast<uint16_t*>(p.C),
+                    p.ldc,
+                    static_cast<int>(p.M),
+                    static_cast<int>(p.N),
+                    static_cast<int>(row_bytes),
+                    static_cast<int>(scale_tiles(p.K)),
+                    static_cast<int>(stages),
+                    static_cast<int>(tiles_m),
+                    p.dtype,
+                    p.act,
+                    d.status,
+                    d.timeout_ns};
+  Launch l(dim3(static_cast<unsigned>(tiles * splits)), dim3(kThreads), Cfg::kSmemBytes, p.stream);
+  l.cluster(static_cast<unsigned>(splits));
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tB, tA, a);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+template <int FMT>
+int launch_rows(const MxGemmProblem& p, const DeviceCtx& d) {
+  if (p.M <= 16) return launch<FMT, 16>(p, d);
+  if (p.M <= 32) return launch<FMT, 32>(p, d);
+  if (p.M <= 64) return launch<FMT, 64>(p, d);
+  return launch<FMT, 128>(p, d);
+}
+
+template <class T>
+__global__ void bias_fill_kernel(uint16_t* C, const uint16_t* bias, int64_t M, int64_t N,
+                                 int64_t ldc, int act) {
+  const int64_t total = M * N;
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / N, c = i - r * N;
+    const float b = bias != nullptr ? unpack2<T>(bias[c]).x : 0.0f;
+    const float2 y = finish2(make_float2(b, b), make_float2(0.0f, 0.0f), act);
+    C[r * ldc + c] = static_cast<uint16_t>(pack2<T>(y.x, y.x));
+  }
+}
+
+}  // namespace
+
+int launch_mx_split_gemm(const MxGemmProblem& p, const DeviceCtx& d) {
+  return p.format == MX_FP8 ? launch_rows<MX_FP8>(p, d) : launch_rows<MX_FP4>(p, d);
+}
+
+int launch_mx_bias_fill(const MxGemmProblem& p) {
+  const int64_t blocks = (p.M * p.N + 255) / 256;
+  Launch l(dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, p.stream);
+  uint16_t* c = static_cast<uint16_t*>(p.C);
+  const uint16_t* b = static_cast<const uint16_t*>(p.bias);
+  const cudaError_t e = p.dtype == MX_F16 ? cudaLaunchKernelEx(&l.cfg, bias_fill_kernel<__half>, c,
+                                                               b, p.M, p.N, p.ldc, p.act)
+                                          : cudaLaunchKernelEx(&l.cfg,
+                                                               bias_fill_kernel<__nv_bfloat16>, c,
+                                                               b, p.M, p.N, p.ldc, p.act);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // namespace mx
+}  // namespace ttc

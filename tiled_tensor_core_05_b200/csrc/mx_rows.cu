@@ -1,0 +1,405 @@
+// The row-wise MX operators: quantisation, its reverse, and the RMS norm with
+// the residual's addition and 16-bit or MX output.  All are bound by device
+// memory: each element is read once and written once.
+#include "mx_common.cuh"
+#include "mx_internal.h"
+
+namespace ttc {
+namespace mx {
+namespace {
+
+// ------------------------------------------------------------------- quantise ---
+// One CTA per 128 x 128 tile of X: 16 threads read a row's 256 bytes, 16 rows
+// at a time, all 8 loads of a thread in flight before the first is used.  A
+// block's maximum is shared by 4 lanes; the tile's 512 scale bytes are
+// collected in shared memory and written as one run.
+constexpr int kTileThreads = 256;
+
+template <class T, int FMT>
+__global__ void __launch_bounds__(kTileThreads)
+    quantize_kernel(const uint16_t* __restrict__ X, uint8_t* __restrict__ Q,
+                    uint8_t* __restrict__ S, int64_t rows, int64_t cols, int64_t ldx, int64_t ldq,
+                    int tiles) {
+  __shared__ uint8_t scales[kTileBytes];
+  const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles));
+  const int64_t rt = blockIdx.x / static_cast<unsigned>(tiles);
+  const int t = threadIdx.x;
+  if (t < kTileBytes / 4) reinterpret_cast<uint32_t*>(scales)[t] = 0;
+  const int q = t & 15;                 // which 8 columns of the tile
+  const int64_t i = 16 * static_cast<int64_t>(kt) + q;
+  const int64_t left = cols - 8 * i;    // elements from here to the row's end
+  const int n = left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left));
+  const int64_t row0 = rt * kTileRows + (t >> 4);
+  grid_dependency_trigger();
+  __syncthreads();
+  grid_dependency_wait();
+  uint4 v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t r = row0 + 16 * j;
+    v[j] = make_uint4(0, 0, 0, 0);
+    if (r < rows && n > 0) v[j] = load8(X + r * ldx + 8 * i, n);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t r = row0 + 16 * j;
+    float y[8];
+    uint32_t e[2];
+    unpack8<T>(v[j], y);
+    const uint32_t byte = quantize8<FMT>(y, e);
+    if (r < rows && n > 0) {
+      store_elements<FMT>(Q + r * ldq, i, e, n);
+      const int rr = (t >> 4) + 16 * j;
+      if ((q & 3) == 0) scales[(rr & 31) * 16 + (rr >> 5) * 4 + (q >> 2)] = static_cast<uint8_t>(byte);
+    }
+  }
+  __syncthreads();
+  if (t < kTileBytes / 16)
+    reinterpret_cast<uint4*>(S + static_cast<int64_t>(blockIdx.x) * kTileBytes)[t] =
+        reinterpret_cast<const uint4*>(scales)[t];
+}
+
+// ----------------------------------------------------------------- dequantise ---
+// The same tile and thread layout; the 4 scales of a row come as one word.
+template <class T, int FMT>
+__global__ void __launch_bounds__(kTileThreads)
+    dequantize_kernel(const uint8_t* __restrict__ Q, const uint8_t* __restrict__ S,
+                      uint16_t* __restrict__ X, int64_t rows, int64_t cols, int64_t ldq,
+                      int64_t ldx, int tiles) {
+  const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles));
+  const int64_t rt = blockIdx.x / static_cast<unsigned>(tiles);
+  const int t = threadIdx.x;
+  const int q = t & 15;
+  const int64_t i = 16 * static_cast<int64_t>(kt) + q;
+  const int64_t left = cols - 8 * i;
+  const int n = left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left));
+  const int64_t row0 = rt * kTileRows + (t >> 4);
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  if (n == 0) return;
+  uint2 e[8];
+  uint32_t byte[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t r = row0 + 16 * j;
+    if (r >= rows) break;
+    byte[j] = S[scale_word(r, kt, tiles) + (q >> 2)];
+    if constexpr (FMT == MX_FP8) {
+      const uint8_t* p = Q + r * ldq + 8 * i;
+      if (n == 8) {
+        e[j] = *reinterpret_cast<const uint2*>(p);
+      } else {
+        uint64_t w = 0;
+        for (int b = 0; b < n; ++b) w |= static_cast<uint64_t>(p[b]) << (8 * b);
+        e[j] = make_uint2(static_cast<uint32_t>(w), static_cast<uint32_t>(w >> 32));
+      }
+    } else {
+      const uint8_t* p = Q + r * ldq + 4 * i;
+      e[j].y = 0;
+      if (n >= 7) {
+        e[j].x = *reinterpret_cast<const uint32_t*>(p);
+      } else {
+        e[j].x = 0;
+        for (int b = 0; 2 * b < n; ++b) e[j].x |= static_cast<uint32_t>(p[b]) << (8 * b);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t r = row0 + 16 * j;
+    if (r >= rows) break;
+    float f[8];
+    if constexpr (FMT == MX_FP8) {
+      const float2 a = from_e4m3x2(e[j].x), b = from_e4m3x2(e[j].x >> 16);
+      const float2 c = from_e4m3x2(e[j].y), d = from_e4m3x2(e[j].y >> 16);
+      f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+      f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
+    } else {
+      from_e2m1x8(e[j].x, f);
+    }
+    const float x = scale_value(byte[j]);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) f[b] *= x;  // exact unless the product leaves fp32's range
+    store8(X + r * ldx + 8 * i, pack8<T>(f), n);
+  }
+}
+
+// ------------------------------------------------------------------- RMS norm ---
+// y = h s w, s = 1 / sqrt(mean(h^2) + eps), h = X or X + R rounded to T.
+//
+// blockDim.x threads share a row, each with the 16-byte vectors threadIdx.x +
+// v blockDim.x of it (V of them in registers; V = 0 reads h twice), so that 4
+// consecutive lanes hold a block of 32.
+//
+// Precision: an MX element is decided by rounding at half steps, where the
+// last bits of y matter.  h^2 and h w are exact in fp32 (products of two
+// 16-bit values); the squares are summed with their rounding errors (two-sum)
+// and then in fp64; s is split into two fp32 numbers.  y is rounded to odd
+// (truncated, the last bit set when anything was cut off), which the rounding
+// to fewer bits that follows cannot tell from the exact value: every output
+// is the formula's value rounded once, up to about 2^-45 relative.  It costs
+// about ten packed instructions per element pair, hidden behind the loads.
+struct NormArgs {
+  const uint16_t *X, *R, *W;
+  uint16_t* H;
+  void* Y;
+  uint8_t* S;
+  int64_t rows, cols, ldx, ldr, ldh, ldy;
+  float eps;
+};
+
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  return __ffma2_rn(b, make_float2(-1.0f, -1.0f), a);
+}
+
+// acc + err += v^2, pair by pair, with the rounding error of each sum kept.
+__device__ __forceinline__ void add_square(float2& acc, float2& err, float2 v) {
+  const float2 q = __fmul2_rn(v, v);
+  const float2 s = __fadd2_rn(acc, q);
+  const float2 b = sub2(s, acc);
+  err = __fadd2_rn(err, __fadd2_rn(sub2(acc, sub2(s, b)), sub2(q, b)));
+  acc = s;
+}
+
+// p (sh + sl) rounded to odd in fp32.  The residual of p sh (exact, by fma)
+// and p sl together can pass half a step, so they are added in and the
+// remainder taken (fast two-sum) before the truncation is decided.
+__device__ __forceinline__ float scale_odd(float p, float sh, float sl) {
+  const float a = p * sh;
+  const float r = fmaf(p, sl, fmaf(p, sh, -a));
+  const float y = a + r;
+  const float e = r - (y - a);
+  uint32_t b = __float_as_uint(y);
+  if (e != 0.0f) b = (b - ((e < 0.0f) != (y < 0.0f) ? 1u : 0u)) | 1u;
+  // a zero with its sign, an infinity and NaN as they are
+  return a != 0.0f && fabsf(a) < __uint_as_float(0x7F800000u) ? __uint_as_float(b) : a;
+}
+
+template <class T>
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
+  float x[8], y[8];
+  unpack8<T>(a, x);
+  unpack8<T>(b, y);
+#pragma unroll
+  // rounding the fp32 sum again to 11 or 8 bits is the same as rounding once
+  // (24 >= 2 * 11 + 2)
+  for (int i = 0; i < 8; ++i) x[i] += y[i];
+  return pack8<T>(x);
+}
+
+template <class T, int FMT, int V>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
+  __shared__ double part[32];
+  const int tpr = blockDim.x;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = row < a.rows;
+  const int64_t tiles = scale_tiles(a.cols);
+  // vectors a thread walks over: all of the row's 128-column tiles
+  const int steps = V > 0 ? V : static_cast<int>((16 * tiles + tpr - 1) / tpr);
+  const uint16_t* x = a.X + row * a.ldx;
+  const uint16_t* r = a.R != nullptr ? a.R + row * a.ldr : nullptr;
+  uint16_t* h = a.H != nullptr ? a.H + row * a.ldh : nullptr;
+  auto count = [&](int64_t i) {
+    const int64_t left = live ? a.cols - 8 * i : 0;
+    return left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left));
+  };
+  grid_dependency_trigger();
+  grid_dependency_wait();
+
+  uint4 hv[V > 0 ? V : 1];
+  float2 acc = make_float2(0.0f, 0.0f), err = make_float2(0.0f, 0.0f);
+  auto squares = [&](const uint4& v) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add_square(acc, err, unpack2<T>(w[k]));
+  };
+  if constexpr (V > 0) {
+    uint4 rv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
+      const int n = count(i);
+      hv[v] = rv[v] = make_uint4(0, 0, 0, 0);
+      if (n > 0) {
+        hv[v] = load8(x + 8 * i, n);
+        if (r != nullptr) rv[v] = load8(r + 8 * i, n);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (r != nullptr) {
+        const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
+        const int n = count(i);
+        hv[v] = add8<T>(hv[v], rv[v]);
+        if (h != nullptr && n > 0) store8(h + 8 * i, hv[v], n);
+      }
+      squares(hv[v]);
+    }
+  } else {
+    for (int v = 0; v < steps; ++v) {
+      const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
+      const int n = count(i);
+      if (n == 0) continue;
+      uint4 u = load8(x + 8 * i, n);
+      if (r != nullptr) {
+        u = add8<T>(u, load8(r + 8 * i, n));
+        if (h != nullptr) store8(h + 8 * i, u, n);
+      }
+      squares(u);
+    }
+  }
+  // an infinite sum has no rounding error (inf - inf is not one)
+  double sum = (isinf(acc.x) || isinf(acc.y))
+                   ? static_cast<double>(acc.x) + static_cast<double>(acc.y)
+                   : (static_cast<double>(acc.x) + static_cast<double>(acc.y)) +
+                         (static_cast<double>(err.x) + static_cast<double>(err.y));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int wpr = tpr >> 5;
+  if (wpr > 1) {
+    double* mine = part + threadIdx.y * wpr;
+    if (lane == 0) mine[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0.0;
+    for (int w = 0; w < wpr; ++w) sum += mine[w];
+  }
+  const double s = 1.0 / sqrt(sum / static_cast<double>(a.cols) + static_cast<double>(a.eps));
+  const float sh = static_cast<float>(s);
+  const float sl = static_cast<float>(s - static_cast<double>(sh));
+
+  auto emit = [&](int64_t i, const uint4& u) {
+    const int n = count(i);
+    float f[8], w[8];
+    unpack8<T>(u, f);
+    uint4 wv = make_uint4(0, 0, 0, 0);
+    if (n > 0) wv = load8(a.W + 8 * i, n);
+    unpack8<T>(wv, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = n > 0 ? scale_odd(f[k] * w[k], sh, sl) : 0.0f;
+    if (n < 8) {  // past the row's end: 0 whatever s is
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k >= n) f[k] = 0.0f;
+    }
+    if constexpr (FMT == MX_NONE) {
+      if (n > 0) store8(static_cast<uint16_t*>(a.Y) + row * a.ldy + 8 * i, pack8<T>(f), n);
+    } else {
+      uint32_t q[2];
+      uint32_t word = quantize8<FMT>(f, q) << (8 * ((lane >> 2) & 3));
+      if (n > 0) store_elements<FMT>(static_cast<uint8_t*>(a.Y) + row * a.ldy, i, q, n);
+      // the 4 blocks of a 128-column tile are 16 lanes: their bytes make a word
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      word |= __shfl_xor_sync(0xffffffffu, word, 8);
+      if ((lane & 15) == 0 && live && (i >> 4) < tiles)
+        *reinterpret_cast<uint32_t*>(a.S + scale_word(row, i >> 4, tiles)) = word;
+    }
+  };
+  if constexpr (V > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) emit(threadIdx.x + static_cast<int64_t>(v) * tpr, hv[v]);
+  } else {
+    for (int v = 0; v < steps; ++v) {
+      const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
+      const int n = count(i);
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (n > 0) {
+        if (r != nullptr && h != nullptr) {
+          u = load8(h + 8 * i, n);  // written by this thread above
+        } else {
+          u = load8(x + 8 * i, n);
+          if (r != nullptr) u = add8<T>(u, load8(r + 8 * i, n));
+        }
+      }
+      emit(i, u);
+    }
+  }
+  if constexpr (FMT != MX_NONE) {
+    // the rows that the last scale tile has no row for: row k of the n that
+    // it has clears places k + n, k + 2n, ...
+    const int64_t first = row & ~static_cast<int64_t>(kTileRows - 1);
+    const int64_t have = a.rows - first;
+    if (live && have < kTileRows)
+      for (int64_t p = row + have; p < first + kTileRows; p += have)
+        for (int64_t kt = threadIdx.x; kt < tiles; kt += tpr)
+          *reinterpret_cast<uint32_t*>(a.S + scale_word(p, kt, tiles)) = 0;
+  }
+}
+
+template <class T, int FMT>
+int run_norm(const NormProblem& p) {
+  const NormArgs a{static_cast<const uint16_t*>(p.X), static_cast<const uint16_t*>(p.R),
+                   static_cast<const uint16_t*>(p.W), static_cast<uint16_t*>(p.H), p.Y,
+                   static_cast<uint8_t*>(p.S), p.rows, p.cols, p.ldx, p.ldr, p.ldh, p.ldy, p.eps};
+  const int64_t vecs = 16 * scale_tiles(p.cols);  // vectors of a row, in whole scale tiles
+  // two vectors a thread up to 512 threads, then four up to 1024; beyond 32768
+  // columns a row is read twice (the second time mostly from L2)
+  int tpr = 32;
+  while (tpr < 512 && 2 * tpr < vecs) tpr *= 2;
+  if (2 * tpr < vecs) tpr = 1024;
+  const int per_cta = tpr < 256 ? 256 / tpr : 1;
+  const int rows_per_cta = static_cast<int>(p.rows < per_cta ? p.rows : per_cta);
+  const int64_t grid = (p.rows + rows_per_cta - 1) / rows_per_cta;
+  Launch l(dim3(static_cast<unsigned>(grid)),
+           dim3(static_cast<unsigned>(tpr), static_cast<unsigned>(rows_per_cta)), 0, p.stream);
+  cudaError_t e;
+  if (vecs <= 2 * tpr)
+    e = cudaLaunchKernelEx(&l.cfg, rms_norm_kernel<T, FMT, 2>, a);
+  else if (vecs <= 4 * tpr)
+    e = cudaLaunchKernelEx(&l.cfg, rms_norm_kernel<T, FMT, 4>, a);
+  else
+    e = cudaLaunchKernelEx(&l.cfg, rms_norm_kernel<T, FMT, 0>, a);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+template <class T, int FMT>
+int run_convert(const ConvertProblem& p, bool to_mx) {
+  const int64_t tiles = scale_tiles(p.cols);
+  const int64_t grid = tiles * ((p.rows + kTileRows - 1) / kTileRows);
+  if (grid > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+  Launch l(dim3(static_cast<unsigned>(grid)), dim3(kTileThreads), 0, p.stream);
+  uint16_t* x = static_cast<uint16_t*>(const_cast<void*>(p.X));
+  uint8_t* q = static_cast<uint8_t*>(const_cast<void*>(p.Q));
+  uint8_t* s = static_cast<uint8_t*>(const_cast<void*>(p.S));
+  const cudaError_t e =
+      to_mx ? cudaLaunchKernelEx(&l.cfg, quantize_kernel<T, FMT>,
+                                 static_cast<const uint16_t*>(x), q, s, p.rows, p.cols, p.ldx,
+                                 p.ldq, static_cast<int>(tiles))
+            : cudaLaunchKernelEx(&l.cfg, dequantize_kernel<T, FMT>,
+                                 static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s),
+                                 x, p.rows, p.cols, p.ldq, p.ldx, static_cast<int>(tiles));
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+template <class T>
+int convert_format(const ConvertProblem& p, bool to_mx) {
+  return p.format == MX_FP8 ? run_convert<T, MX_FP8>(p, to_mx) : run_convert<T, MX_FP4>(p, to_mx);
+}
+
+template <class T>
+int norm_format(const NormProblem& p) {
+  switch (p.format) {
+    case MX_FP8: return run_norm<T, MX_FP8>(p);
+    case MX_FP4: return run_norm<T, MX_FP4>(p);
+    default: return run_norm<T, MX_NONE>(p);
+  }
+}
+
+}  // namespace
+
+int launch_quantize(const ConvertProblem& p) {
+  return p.dtype == MX_F16 ? convert_format<__half>(p, true)
+                           : convert_format<__nv_bfloat16>(p, true);
+}
+
+int launch_dequantize(const ConvertProblem& p) {
+  return p.dtype == MX_F16 ? convert_format<__half>(p, false)
+                           : convert_format<__nv_bfloat16>(p, false);
+}
+
+int launch_rms_norm(const NormProblem& p) {
+  return p.dtype == MX_F16 ? norm_format<__half>(p) : norm_format<__nv_bfloat16>(p);
+}
+
+}  // namespace mx
+}  // namespace ttc

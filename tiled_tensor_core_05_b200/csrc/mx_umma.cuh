@@ -1,0 +1,97 @@
+// tcgen05 helpers of the MX products (block-scaled MMA, scale factors in
+// TMEM), in the manner of sm100.cuh.
+//
+// An operand stage is 128 bytes of each row (128 E4M3 or 256 E2M1 elements) in
+// the 128-byte-swizzled K-major layout, and the matching scale tiles (one of
+// 512 bytes per 128 elements and 128 rows) as they lie in memory.  One MMA
+// takes 32 bytes of K: 32 E4M3 elements = one scale a row, or 64 E2M1
+// elements = two.
+#pragma once
+
+#include "mx_common.cuh"
+
+namespace ttc {
+namespace mx {
+
+template <int FMT>
+struct Kind {
+  static constexpr int kStageK = FMT == MX_FP8 ? 128 : 256;  // elements per stage
+  static constexpr int kSfTiles = FMT == MX_FP8 ? 1 : 2;     // scale tiles per stage
+  static constexpr int kSfCols = 4 * kSfTiles;               // TMEM columns of a stage's scales
+};
+constexpr int kRowBytes = 128;  // bytes of a row in a stage
+constexpr int kMmaBytes = 32;   // bytes of a row that one MMA takes
+constexpr int kMmasPerStage = kRowBytes / kMmaBytes;
+
+// Instruction descriptor of the block-scaled kinds.
+//   bits 4-5 scale-factor id of B, 7-9 A format, 10-12 B format, 17-22 N >> 3,
+//   23 scale type (1 = UE8M0), 27-28 M >> 7, 29-30 scale-factor id of A;
+//   A and B K-major.  E4M3 is 0 of kind::mxf8f6f4, E2M1 is 1 of kind::mxf4.
+// The scale-factor id names the byte of each 32-bit scale word to start from.
+template <int FMT>
+__host__ __device__ constexpr uint32_t mx_idesc(int m, int n, int k) {
+  const uint32_t f = FMT == MX_FP8 ? 0u : 1u;
+  const uint32_t id = FMT == MX_FP8 ? static_cast<uint32_t>(k) : 2u * static_cast<uint32_t>(k & 1);
+  return (id << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(m >> 7) << 27) | (id << 29);
+}
+
+// Descriptor of a scale tile: 32 rows of 16 bytes, no swizzle, 8-row groups
+// 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(128u >> 4) << 32 |
+         static_cast<uint64_t>(1u) << 46;
+}
+
+// A scale tile from shared memory to 4 TMEM columns, repeated in the four
+// 32-lane quarters: lane l, column c holds the scales of row 32 c + l.
+template <int CTAS>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (CTAS == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+// D (+)= (A . SA) (B . SB), fp32 accumulator.
+#define TTC_MX_MMA(GROUP, KIND)                                                                   \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                  \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;" \
+               "\n\t}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)  \
+               : "memory")
+template <int FMT, int CTAS>
+__device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  if constexpr (FMT == MX_FP8 && CTAS == 1)
+    TTC_MX_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
+  else if constexpr (FMT == MX_FP8)
+    TTC_MX_MMA("2", "mxf8f6f4.block_scale.scale_vec::1X");
+  else if constexpr (CTAS == 1)
+    TTC_MX_MMA("1", "mxf4.block_scale.scale_vec::2X");
+  else
+    TTC_MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
+}
+#undef TTC_MX_MMA
+
+// Untiled copy of `bytes` (a multiple of 16) global -> shared, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// bias + activation in fp32 of two columns.
+__device__ __forceinline__ float2 finish2(float2 v, float2 b, int act) {
+  v = __fadd2_rn(v, b);
+  return act == kActRelu   ? activate2<kActRelu>(v)
+         : act == kActGelu ? activate2<kActGelu>(v)
+                           : v;
+}
+
+}  // namespace mx
+}  // namespace ttc
