@@ -257,6 +257,12 @@ SHAPES = [(1, 1, 1), (1, 128, 32), (2, 130, 33), (16, 128, 256), (17, 100, 100),
           (40, 130, 16385)]
 
 
+# enough 256 x 256 tiles for the CTA-pair kernel: one wave and several, ragged
+# rows and columns, K of a part of a k-block, of one and of many
+LARGE = [(1300, 2100, 70), (1500, 1700, 513), (2600, 2601, 1100), (4100, 1000, 260),
+         (300, 9000, 4111)]
+
+
 def exact_operand(rng, rows, cols, fmt):
     """Codes and scales whose products sum exactly in 24 bits."""
     if fmt == "mxfp4":
@@ -269,7 +275,7 @@ def exact_operand(rng, rows, cols, fmt):
     return codes, scales
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + LARGE)
 @pytest.mark.parametrize("fmt", ref.FORMATS)
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_product_of_exact_sums(M, N, K, fmt, dtype):
@@ -296,7 +302,7 @@ def random_operand(rng, rows, cols, fmt, scale):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 300, 700), (20, 200, 1000), (50, 129, 515), (100, 128, 2000),
-                                   (300, 400, 1100)])
+                                   (300, 400, 1100), (1601, 1500, 640)])
 @pytest.mark.parametrize("fmt", ref.FORMATS)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("act", ["none", "relu", "gelu"])
@@ -313,7 +319,7 @@ def test_product(M, N, K, fmt, dtype, act, bias):
     assert (err <= off * (1 + ref.HALF[t]) + ref.HALF[t] * np.abs(want) + ref.TINY[t]).all()
 
 
-@pytest.mark.parametrize("M", [1, 40, 200])
+@pytest.mark.parametrize("M", [1, 40, 200, 12000])
 @pytest.mark.parametrize("fmt", ref.FORMATS)
 @pytest.mark.parametrize("side", ["a", "b"])
 def test_nan_blocks_stay_in_their_row(M, fmt, side):
@@ -331,7 +337,7 @@ def test_nan_blocks_stay_in_their_row(M, fmt, side):
     assert np.array_equal(ref.to_np(got), ref.round_to(want, torch.float16), equal_nan=True)
 
 
-@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("M", [3, 300, 12000])
 def test_scales_from_end_to_end(M):
     """Scales far from 1 on both sides that cancel: 2^60 against 2^-60, and the smallest."""
     rng = np.random.default_rng(2)

@@ -182,6 +182,20 @@ int encode_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64
   return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_ARG;
 }
 
+int encode_tmap_scales(CUtensorMap* map, const void* base, uint64_t tiles, uint32_t box_tiles) {
+  load_entry_points();
+  if (g_encode == nullptr) return GEMM_ERR_LAUNCH;
+  const cuuint64_t dims[2] = {128, tiles};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {128, box_tiles};
+  const cuuint32_t estrides[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(base), dims,
+                              strides, box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
 bool pdl_enabled() {
   static const bool on = [] {
     const char* s = std::getenv("TTC_PDL");

@@ -99,6 +99,10 @@ int encode_tmap_f16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint6
 int encode_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                       uint64_t ld, uint32_t box_outer);
 
+// Scale tiles of 512 bytes, one after the other: boxes of box_tiles tiles, no
+// swizzle; the innermost coordinate is always 0.
+int encode_tmap_scales(CUtensorMap* map, const void* base, uint64_t tiles, uint32_t box_tiles);
+
 // Large-shape path: persistent warp-specialised tcgen05 kernel, one SM per
 // 128 x block_n tile (GEMM_PATH_TILE), or a pair of SMs per 256 x 256
 // (GEMM_PATH_TILE_PAIR) or 512 x 256 (GEMM_PATH_TILE_PAIR_TALL) tile

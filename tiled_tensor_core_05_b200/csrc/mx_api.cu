@@ -96,7 +96,10 @@ int run_gemm(const MxGemmProblem& p) {
   rc = check_mx(p.A, p.SA, p.M, p.K, p.lda, p.format, d.device);
   if (rc == GEMM_OK) rc = check_mx(p.B, p.SB, p.N, p.K, p.ldb, p.format, d.device);
   if (rc != GEMM_OK) return rc;
-  return launch_mx_split_gemm(p, d);
+  // 256 x 256 tiles of a CTA pair once there are enough of them
+  const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+  return p.M > 128 && tiles >= d.sm_count / 4 ? launch_mx_pair_gemm(p, d)
+                                              : launch_mx_split_gemm(p, d);
 }
 
 }  // namespace

@@ -1,0 +1,407 @@
+// C = act(A B^T + bias) for MX operands, large shapes: a CTA pair per 256 x 256
+// tile of C, persistent, the block-scaled tcgen05.mma.cta_group::2.
+//
+// The arrangement is that of the fp16 pair kernel in gemm_tile.cu (TMA
+// producer, one MMA thread for both SMs, epilogue warps, grouped raster, every
+// other wave sweeping K downwards); what differs is what the scales need:
+//
+//   * Each CTA stages 128 bytes of 128 rows of A and of 128 rows of B per
+//     k-block, the scale tiles of its own rows of A, and those of all 256
+//     rows of B (each SM scales its half of the rows of D by all columns).
+//   * Per k-block the MMA thread copies the scale tiles of both SMs from
+//     shared memory to TMEM (tcgen05.cp), then issues 4 MMAs.  kSets sets of
+//     scale columns alternate; a set is overwritten only after the MMAs that
+//     read it have completed (the empty barrier of their ring stage).
+//   * TMEM holds 512 columns: two accumulators of 256 and the scales do not
+//     fit, so the accumulators share kOverlap columns: buffer 0 is columns
+//     0..255, buffer 1 ends where the scales begin.  The epilogue of a tile
+//     reads the shared columns first and hands them back at once, so the next
+//     tile's MMAs wait for one 64-column read instead of a whole epilogue.
+#include "mx_internal.h"
+#include "mx_umma.cuh"
+#include "tile_common.cuh"
+
+namespace ttc {
+namespace mx {
+namespace {
+
+constexpr int kTile = 256;      // rows and columns of a pair's tile
+constexpr int kHalf = 128;      // rows of A and of B per CTA
+constexpr int kStages = 5;
+constexpr int kEpiWarps = 8;    // two per TMEM lane quarter, half of the columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kPanelRows = 4096;  // rows of A per raster panel
+
+template <int FMT>
+struct PairCfg {
+  static constexpr int kOperand = kHalf * kRowBytes;  // bytes of A, and of B, per stage
+  static constexpr int kSf = Kind<FMT>::kSfTiles * kTileBytes;  // scales of 128 rows
+  static constexpr int kStageBytes = 2 * kOperand + 3 * kSf;
+  static constexpr int kBars = 2 * kStages + 6;
+  static constexpr int kSmemBytes =
+      1024 + kStages * kStageBytes + kEpiWarps * kEpiBuf + kBars * 8 + 16;
+  static constexpr int kSetCols = 3 * Kind<FMT>::kSfCols;  // scale columns of a k-block
+  static constexpr int kSets = 48 / kSetCols;
+  static constexpr int kSfBase = 512 - 48;
+  static constexpr int kAcc1 = kSfBase - kTile;  // first column of buffer 1
+  static constexpr int kOverlap = kTile - kAcc1;
+  static_assert(kSets >= 2 && kOverlap <= kEpiCols, "TMEM columns");
+  static_assert(kSmemBytes <= kMaxDynamicSmem, "shared memory budget");
+};
+
+struct PairArgs {
+  uint16_t* C;
+  const uint16_t* bias;
+  int64_t ldc;
+  int M, N;
+  int row_bytes, sf_tiles, num_kb;
+  int group_m;
+  int* status;
+  uint64_t timeout_ns;
+};
+
+// 64 fp32 accumulator columns of this thread's row -> 32 packed 16-bit pairs.
+template <class T, int ACT>
+__device__ __forceinline__ void convert(const uint32_t (&v)[64], const uint16_t* bias, int col0,
+                                        int N, uint32_t (&h)[32]) {
+  uint32_t bb[32];
+  if (bias != nullptr) load_bias_chunk(reinterpret_cast<const __half*>(bias), col0, N, bb);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    if (bias != nullptr) x = __fadd2_rn(x, unpack2<T>(bb[i]));
+    x = activate2<ACT>(x);
+    h[i] = pack2<T>(x.x, x.y);
+  }
+}
+
+template <int FMT, class T, int ACT>
+__global__ void __launch_bounds__(kThreads, 1)
+    pair_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmSA,
+                     const __grid_constant__ CUtensorMap tmSB,
+                     const __grid_constant__ CUtensorMap tmC, const PairArgs a) {
+  using Cfg = PairCfg<FMT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* smA = smem;
+  uint8_t* smB = smA + kStages * Cfg::kOperand;
+  uint8_t* smEpi = smB + kStages * Cfg::kOperand;
+  uint8_t* smS = smEpi + kEpiWarps * kEpiBuf;  // per stage: scales of A, of B's two halves
+  uint64_t* full = reinterpret_cast<uint64_t*>(smS + kStages * 3 * Cfg::kSf);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;     // [2] a buffer has been read
+  uint64_t* shared_empty = acc_empty + 2; // the columns both buffers share have been read
+  uint64_t* drain = shared_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Cfg::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(cluster_id_x());
+  const int npairs = static_cast<int>(num_clusters_x());
+  const int num_m = (a.M + kTile - 1) / kTile;
+  const int num_n = (a.N + kTile - 1) / kTile;
+  const int num_tiles = num_m * num_n;
+  const int n8 = a.N & ~7;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(shared_empty, kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_alloc_permit_pair();
+  }
+  tc_fence_before_sync();
+  cluster_sync();  // barriers of both CTAs initialised, TMEM of both SMs allocated
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  const uint32_t full_leader = map_to_cta(smem_u32(full), 0);
+  const uint32_t acc_empty_leader = map_to_cta(smem_u32(acc_empty), 0);
+  const uint32_t shared_empty_leader = map_to_cta(smem_u32(shared_empty), 0);
+
+  if (warp == 0) {
+    // --------------------------------------------- TMA producer (both CTAs) ---
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, parity = 0, down = 0;
+      bool ok = true;
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs, down ^= 1u) {
+        int mb, nb;
+        tile_coords(tile, num_m, num_n, a.group_m, mb, nb);
+        const int a_row = mb * kTile + rank * kHalf;
+        const int b_row = nb * kTile + rank * kHalf;
+        for (int i = 0; i < a.num_kb; ++i) {
+          const int kb = down ? a.num_kb - 1 - i : i;
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kStageBytes);
+          const uint32_t bar = full_leader + stage * 8;
+          const int kt = kb * Kind<FMT>::kSfTiles;
+          uint8_t* sf = smS + stage * 3 * Cfg::kSf;
+          tma_load_2d_pair(&tmA, bar, smA + stage * Cfg::kOperand, kb * kRowBytes, a_row);
+          tma_load_2d_pair(&tmB, bar, smB + stage * Cfg::kOperand, kb * kRowBytes, b_row);
+          // past the last row of tiles these read another row's or zeros: the
+          // rows and columns they scale are not stored
+          tma_load_2d_pair(&tmSA, bar, sf, 0, (2 * mb + rank) * a.sf_tiles + kt);
+          tma_load_2d_pair(&tmSB, bar, sf + Cfg::kSf, 0, 2 * nb * a.sf_tiles + kt);
+          tma_load_2d_pair(&tmSB, bar, sf + 2 * Cfg::kSf, 0, (2 * nb + 1) * a.sf_tiles + kt);
+          armed |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleProducer << 4) | 3);
+        if (leader) {
+          for (int s = 0; s < kStages; ++s)
+            if (armed & (1u << s))
+              (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
+        } else {
+          // this CTA's loads complete on the leader's barriers, which it cannot
+          // poll; give loads already issued ample time to land
+          spin_ns(2000000);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------- MMA issuer (leader) ---
+    if (leader && lane == 0) {
+      int stage = 0, old_stage = 0;  // ring stage of this k-block, and of the one kSets before
+      uint32_t phase = 0, old_phase = 0, down = 0;
+      int buf = 0, set = 0;
+      uint32_t acc_phase = 0, shared_phase = 0;
+      int64_t issued = 0;  // k-blocks so far
+      bool ok = true;
+      int site = 0;
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs, down ^= 1u) {
+        if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, a.timeout_ns)) {
+          ok = false;
+          site = 5;
+          break;
+        }
+        if (tile != pair) {  // the previous tile's epilogue has read the shared columns
+          if (!mbar_wait(shared_empty, shared_phase, abort_flag, a.timeout_ns)) {
+            ok = false;
+            site = 7;
+            break;
+          }
+          shared_phase ^= 1u;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + static_cast<uint32_t>(buf ? Cfg::kAcc1 : 0);
+        for (int i = 0; i < a.num_kb; ++i) {
+          const int kb = down ? a.num_kb - 1 - i : i;
+          if (!mbar_wait(&full[stage], phase, abort_flag, a.timeout_ns)) {
+            ok = false;
+            site = 6;
+            break;
+          }
+          if (issued >= Cfg::kSets) {  // the MMAs that read this set of scales are done
+            if (!mbar_wait(&empty[old_stage], old_phase, abort_flag, a.timeout_ns)) {
+              ok = false;
+              site = 8;
+              break;
+            }
+            if (++old_stage == kStages) {
+              old_stage = 0;
+              old_phase ^= 1u;
+            }
+          }
+          ++issued;
+          tc_fence_after_sync();
+          const uint32_t a_addr = smem_u32(smA + stage * Cfg::kOperand);
+          const uint32_t b_addr = smem_u32(smB + stage * Cfg::kOperand);
+          const uint32_t s_addr = smem_u32(smS + stage * 3 * Cfg::kSf);
+          // columns: 4 per tile of A's scales, then 8 per tile of B's (256 rows)
+          const uint32_t sfa = tmem + Cfg::kSfBase + static_cast<uint32_t>(set * Cfg::kSetCols);
+          const uint32_t sfb = sfa + Kind<FMT>::kSfCols;
+#pragma unroll
+          for (int t = 0; t < Kind<FMT>::kSfTiles; ++t) {
+            copy_scales<2>(sfa + 4 * t, scale_desc(s_addr + t * kTileBytes));
+            copy_scales<2>(sfb + 8 * t, scale_desc(s_addr + Cfg::kSf + t * kTileBytes));
+            copy_scales<2>(sfb + 8 * t + 4, scale_desc(s_addr + 2 * Cfg::kSf + t * kTileBytes));
+          }
+          const int left = a.row_bytes - kb * kRowBytes;
+#pragma unroll
+          for (int k = 0; k < kMmasPerStage; ++k) {
+            if (k * kMmaBytes >= left) break;
+            const int t = FMT == MX_FP8 ? 0 : k / 2;
+            mx_mma<FMT, 2>(d, smem_desc_sw128(a_addr + k * kMmaBytes, 16, 1024),
+                           smem_desc_sw128(b_addr + k * kMmaBytes, 16, 1024),
+                           mx_idesc<FMT>(kTile, kTile, k), sfa + 4 * t, sfb + 8 * t,
+                           (i | k) != 0 ? 1u : 0u);
+          }
+          umma_commit_pair(&empty[stage], 0x3);  // stage free in both CTAs
+          if (++set == Cfg::kSets) set = 0;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(&acc_full[buf], 0x3);  // both epilogues may read
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
+      }
+      if (!ok) {
+        raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleMma << 4) | site);
+        umma_commit_pair(drain, 0x1);
+        (void)mbar_wait(drain, 0, nullptr, a.timeout_ns);
+      }
+    }
+  } else {
+    // ------------------------------------------------ epilogue (both CTAs) ---
+    const int q = warp & 3;
+    const int ew = warp - 2;
+    const int g = ew >> 2;  // columns 128 g .. 128 g + 127 of the tile
+    uint8_t* box = smEpi + ew * kEpiBuf;
+    int buf = 0;
+    uint32_t acc_phase = 0, chunk_no = 0;
+    for (int tile = pair; tile < num_tiles; tile += npairs) {
+      int mb, nb;
+      tile_coords(tile, num_m, num_n, a.group_m, mb, nb);
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait(&acc_full[buf], acc_phase, abort_flag, a.timeout_ns) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        if (lane == 0)
+          raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 3);
+        break;
+      }
+      tc_fence_after_sync();
+      const int row0 = mb * kTile + rank * kHalf + q * kEpiRows;
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                             static_cast<uint32_t>(buf ? Cfg::kAcc1 : 0);
+      // shared columns: the last ones of buffer 0, the first ones of buffer 1
+      const int first = buf == 0 && g == 1 ? 1 : 0;
+      const bool has_shared = g == (buf ^ 1);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        const int col = (2 * g + (c ^ first)) * kEpiCols;
+        uint32_t v[64], h[32];
+        tmem_load_32x32b_x64(t_row + col, v);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (c == 0 && has_shared) mbar_arrive_cluster_relaxed(shared_empty_leader);
+          if (c == 1) mbar_arrive_cluster_relaxed(acc_empty_leader + buf * 8);
+        }
+        convert<T, ACT>(v, a.bias, nb * kTile + col, a.N, h);
+        stage_chunk<1>(h, box, chunk_no, &tmC, reinterpret_cast<__half*>(a.C), a.ldc, a.M, a.N, n8,
+                       row0, nb * kTile + col, lane);
+      }
+      buf ^= 1;
+      if (buf == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before_sync();
+  // no CTA of the pair leaves (or frees TMEM) while the other may still signal
+  // its barriers or use its TMEM
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int FMT, class T, int ACT>
+int launch(const MxGemmProblem& p, const DeviceCtx& d) {
+  using Cfg = PairCfg<FMT>;
+  static std::atomic<uint64_t> attr_done{0};
+  static std::atomic<int> max_pairs[64] = {};  // resident pairs, per device (0 = not asked yet)
+  auto kern = pair_gemm_kernel<FMT, T, ACT>;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, d.device, attr_done))
+    return GEMM_ERR_LAUNCH;
+  const int64_t row_bytes = mx_row_bytes(p.K, FMT);
+  const int64_t sf_tiles = scale_tiles(p.K);
+  const uint64_t n8 = static_cast<uint64_t>(p.N) & ~7ull;
+  constexpr int kBox = Kind<FMT>::kSfTiles;
+  CUtensorMap tA, tB, tSA, tSB, tC;
+  int rc = encode_tmap_u8_2d(&tA, p.A, row_bytes, p.M, p.lda, kHalf);
+  if (rc == 0) rc = encode_tmap_u8_2d(&tB, p.B, row_bytes, p.N, p.ldb, kHalf);
+  if (rc == 0) rc = encode_tmap_scales(&tSA, p.SA, (p.M + 127) / 128 * sf_tiles, kBox);
+  if (rc == 0) rc = encode_tmap_scales(&tSB, p.SB, (p.N + 127) / 128 * sf_tiles, kBox);
+  // (the map of C is never used when n8 is 0)
+  if (rc == 0) rc = encode_tmap_f16_2d(&tC, p.C, n8 > 0 ? n8 : 8, p.M, p.ldc, kEpiCols, kEpiRows);
+  if (rc != 0) return rc;
+  Launch l(dim3(2 * (d.sm_count / 2)), dim3(kThreads), Cfg::kSmemBytes, p.stream);
+  l.cluster(2);
+  int resident = max_pairs[d.device & 63].load(std::memory_order_relaxed);
+  if (resident == 0) {
+    if (cudaOccupancyMaxActiveClusters(&resident, kern, &l.cfg) != cudaSuccess || resident <= 0) {
+      cudaGetLastError();
+      resident = d.sm_count / 2;
+    }
+    max_pairs[d.device & 63].store(resident, std::memory_order_relaxed);
+  }
+  const int64_t tiles = ((p.M + kTile - 1) / kTile) * ((p.N + kTile - 1) / kTile);
+  if (tiles > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+  l.cfg.gridDim = dim3(2u * static_cast<unsigned>(tiles < resident ? tiles : resident));
+  const PairArgs a{static_cast<uint16_t*>(p.C),
+                   static_cast<const uint16_t*>(p.bias),
+                   p.ldc,
+                   static_cast<int>(p.M),
+                   static_cast<int>(p.N),
+                   static_cast<int>(row_bytes),
+                   static_cast<int>(sf_tiles),
+                   static_cast<int>((row_bytes + kRowBytes - 1) / kRowBytes),
+                   group_tiles(kPanelRows, kTile, kTile),
+                   d.status,
+                   d.timeout_ns};
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tA, tB, tSA, tSB, tC, a);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+template <int FMT, class T>
+int launch_act(const MxGemmProblem& p, const DeviceCtx& d) {
+  switch (p.act) {
+    case kActRelu: return launch<FMT, T, kActRelu>(p, d);
+    case kActGelu: return launch<FMT, T, kActGelu>(p, d);
+    default: return launch<FMT, T, kActNone>(p, d);
+  }
+}
+
+}  // namespace
+
+int launch_mx_pair_gemm(const MxGemmProblem& p, const DeviceCtx& d) {
+  if (p.format == MX_FP8)
+    return p.dtype == MX_F16 ? launch_act<MX_FP8, __half>(p, d)
+                             : launch_act<MX_FP8, __nv_bfloat16>(p, d);
+  return p.dtype == MX_F16 ? launch_act<MX_FP4, __half>(p, d)
+                           : launch_act<MX_FP4, __nv_bfloat16>(p, d);
+}
+
+}  // namespace mx
+}  // namespace ttc

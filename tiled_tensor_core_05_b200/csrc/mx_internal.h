@@ -38,6 +38,7 @@ int launch_quantize(const ConvertProblem& p);
 int launch_dequantize(const ConvertProblem& p);
 int launch_rms_norm(const NormProblem& p);
 int launch_mx_split_gemm(const MxGemmProblem& p, const DeviceCtx& d);
+int launch_mx_pair_gemm(const MxGemmProblem& p, const DeviceCtx& d);
 // C = act(bias), or act(0) without one: a product over no elements.
 int launch_mx_bias_fill(const MxGemmProblem& p);
 

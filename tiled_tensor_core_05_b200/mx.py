@@ -15,7 +15,6 @@ elements of a row.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -73,8 +72,10 @@ def _round(n: int, to: int) -> int:
 
 def mx_row_bytes(cols: int, format: str) -> int:
     """Bytes of a row of ``cols`` elements."""
+    if format == "mxfp8":
+        return cols
     _format(format)
-    return cols if format == "mxfp8" else (cols + 1) // 2
+    return (cols + 1) // 2
 
 
 def mx_scale_bytes(rows: int, cols: int) -> int:
@@ -87,16 +88,18 @@ class MxTensor:
     of 16 bytes apart, and ``scales`` uint8, flat, in 128 x 4 tiles
     (``mx_tile_scales``)."""
 
-    __slots__ = ("data", "scales", "rows", "cols", "format")
+    __slots__ = ("data", "scales", "rows", "cols", "format", "ld")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
                  format: str):
         need = mx_row_bytes(cols, format)
-        if data.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        if data.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
             raise TypeError("data and scales must be torch.uint8")
-        if data.dim() != 2 or data.shape[0] != rows or data.shape[1] < need:
-            raise ValueError(f"data must be ({rows}, >= {need}), got {tuple(data.shape)}")
-        if data.shape[1] > 1 and data.stride(1) != 1:
+        shape = data.shape
+        if len(shape) != 2 or shape[0] != rows or shape[1] < need:
+            raise ValueError(f"data must be ({rows}, >= {need}), got {tuple(shape)}")
+        step, unit = data.stride()
+        if unit != 1 and shape[1] > 1:
             raise ValueError("the bytes of a row must be contiguous")
         if scales.dim() != 1 or not scales.is_contiguous() or \
                 scales.numel() < mx_scale_bytes(rows, cols):
@@ -105,7 +108,9 @@ class MxTensor:
         if data.device != scales.device:
             raise ValueError("data and scales must be on one device")
         self.data, self.scales = data, scales
-        self.rows, self.cols, self.format = int(rows), int(cols), format
+        self.rows, self.cols, self.format = rows, cols, format
+        # bytes between rows (a single row has no meaningful stride)
+        self.ld = step if rows > 1 else (need + 15) // 16 * 16
 
     @property
     def shape(self) -> tuple[int, int]:
@@ -118,18 +123,15 @@ class MxTensor:
     def __repr__(self):
         return f"MxTensor({self.rows} x {self.cols}, {self.format}, {self.device})"
 
-    def _ld(self) -> int:
-        if self.rows > 1:
-            return int(self.data.stride(0))
-        return _round(mx_row_bytes(self.cols, self.format), 16)
-
 
 def mx_empty(rows: int, cols: int, format: str, device) -> MxTensor:
     """An uninitialised MX matrix."""
-    data = torch.empty((rows, _round(mx_row_bytes(cols, format), 16)), dtype=torch.uint8,
-                       device=device)
-    scales = torch.empty(mx_scale_bytes(rows, cols), dtype=torch.uint8, device=device)
-    return MxTensor(data, scales, rows, cols, format)
+    q = object.__new__(MxTensor)  # right by construction: no checks
+    q.ld = _round(mx_row_bytes(cols, format), 16)
+    q.data = torch.empty((rows, q.ld), dtype=torch.uint8, device=device)
+    q.scales = torch.empty((mx_scale_bytes(rows, cols),), dtype=torch.uint8, device=device)
+    q.rows, q.cols, q.format = rows, cols, format
+    return q
 
 
 def mx_tile_scales(scales: torch.Tensor) -> torch.Tensor:
@@ -149,53 +151,82 @@ def mx_untile_scales(scales: torch.Tensor, rows: int, cols: int) -> torch.Tensor
     return t[:rows, :-(-cols // BLOCK)]
 
 
-def _matrix(t: torch.Tensor, what: str, shape=None, dtype=None, device=None) -> torch.Tensor:
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{what} must be {dtype or 'torch.float16 or torch.bfloat16'}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{what} must be a matrix{'' if shape is None else f' {tuple(shape)}'}, "
-                         f"got {tuple(t.shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{what} must be a CUDA tensor{'' if device is None else f' on {device}'}")
-    return t
+def _dtype(t: torch.Tensor, what: str) -> int:
+    """The code of the 16-bit type of the CUDA tensor ``t``."""
+    code = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        raise TypeError(f"{what} must be a torch.float16 or torch.bfloat16 tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return code
 
 
-def _vector(t: torch.Tensor, what: str, n: int, dtype, device) -> torch.Tensor:
-    if t.dtype != dtype:
+def _matrix(t: torch.Tensor, what: str, shape, dtype, device) -> int:
+    """Checks a matrix; its row stride in elements (of a single row, whose
+    stride means nothing, the columns rounded up to 8)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if t.shape != shape or len(shape) != 2:
+        raise ValueError(f"{what} must be a matrix {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
+    step, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError(f"the columns of {what} must be contiguous (stride(1) == 1)")
+    return step if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+
+
+def _vector(t: torch.Tensor, what: str, n: int, dtype, device) -> int:
+    """Checks a vector; its address."""
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
     if t.numel() != n or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{what} must be {n} contiguous values on {device}")
-    return t
+    return t.data_ptr()
 
 
-def _mx(q: MxTensor, what: str, shape=None, format=None, device=None) -> MxTensor:
+def _mx(q: MxTensor, what: str) -> torch.device:
+    """Checks an MX input; its device."""
     if not isinstance(q, MxTensor):
         raise TypeError(f"{what} must be an MxTensor")
-    if (shape is not None and q.shape != tuple(shape)) or \
-            (format is not None and q.format != format):
-        raise ValueError(f"{what} must be {shape} {format}, got {q!r}")
-    if not q.data.is_cuda or (device is not None and q.device != device):
-        raise ValueError(f"{what} must be on {device or 'a CUDA device'}")
-    return q
+    if not q.data.is_cuda:
+        raise ValueError(f"{what} must be on a CUDA device")
+    return q.data.device
 
 
-def _owner(stream, device):
-    """Context in which outputs are allocated: the stream that writes them."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)
+def _mx_out(q: MxTensor, rows: int, cols: int, format: str, device) -> None:
+    if _mx(q, "out") != device or q.rows != rows or q.cols != cols or q.format != format:
+        raise ValueError(f"out must be ({rows}, {cols}) {format} on {device}, got {q!r}")
 
 
 def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
     """A new matrix whose rows start on 16 bytes."""
+    if cols % 8 == 0:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
     return torch.empty((rows, _round(cols, 8)), dtype=dtype, device=device)[:, :cols]
 
 
-def _call(name: str, device, stream, *args) -> None:
-    with torch.cuda.device(device):
-        ops._check(getattr(mx_lib(), name)(*args, ops._stream_handle(stream, device)), name)
+def _alloc(stream, device, make, *args):
+    """make(*args) with the memory belonging to the stream that will write it."""
+    if stream is None:
+        return make(*args)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
+def _call(name: str, device: torch.device, stream, *args) -> None:
+    """The library call, with ``device`` current, on ``stream`` or the device's
+    current stream."""
+    if torch._C._cuda_getDevice() != device.index:
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
+        ops._stream_handle(stream, device)
+    rc = getattr(_lib or mx_lib(), name)(*args, handle)
+    if rc:
+        ops._check(rc, name)
 
 
 def mx_quantize(x: torch.Tensor, format: str, out: MxTensor | None = None, *,
@@ -205,13 +236,15 @@ def mx_quantize(x: torch.Tensor, format: str, out: MxTensor | None = None, *,
     quotient by its block's scale.  Asynchronous on ``stream`` (default: the
     current stream)."""
     fmt = _format(format)
-    _matrix(x, "x")
-    rows, cols = x.shape
-    with _owner(stream, x.device):
-        out = mx_empty(rows, cols, format, x.device) if out is None else \
-            _mx(out, "out", (rows, cols), format, x.device)
-    _call("mx_quantize", x.device, stream, x.data_ptr(), out.data.data_ptr(),
-          out.scales.data_ptr(), rows, cols, ops._ld_padded(x), out._ld(), _DTYPES[x.dtype], fmt)
+    dtype, dev, shape = _dtype(x, "x"), x.device, x.shape
+    ldx = _matrix(x, "x", shape, x.dtype, dev)
+    rows, cols = shape
+    if out is None:
+        out = _alloc(stream, dev, mx_empty, rows, cols, format, dev)
+    else:
+        _mx_out(out, rows, cols, format, dev)
+    _call("mx_quantize", dev, stream, x.data_ptr(), out.data.data_ptr(), out.scales.data_ptr(),
+          rows, cols, ldx, out.ld, dtype, fmt)
     return out
 
 
@@ -219,16 +252,15 @@ def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float16,
                   out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
     """The values ``q`` stands for, rounded to ``dtype`` (fp16 or bf16; of
     ``out`` when given)."""
-    _mx(q, "q")
+    dev = _mx(q, "q")
     if out is None:
         if dtype not in _DTYPES:
             raise TypeError("dtype must be torch.float16 or torch.bfloat16")
-        with _owner(stream, q.device):
-            out = _new(q.rows, q.cols, dtype, q.device)
-    _matrix(out, "out", q.shape, device=q.device)
-    _call("mx_dequantize", q.device, stream, q.data.data_ptr(), q.scales.data_ptr(),
-          out.data_ptr(), q.rows, q.cols, q._ld(), ops._ld_padded(out), _DTYPES[out.dtype],
-          FORMATS[q.format])
+        out = _alloc(stream, dev, _new, q.rows, q.cols, dtype, dev)
+    code = _dtype(out, "out")
+    ldx = _matrix(out, "out", (q.rows, q.cols), out.dtype, dev)
+    _call("mx_dequantize", dev, stream, q.data.data_ptr(), q.scales.data_ptr(), out.data_ptr(),
+          q.rows, q.cols, q.ld, ldx, code, FORMATS[q.format])
     return out
 
 
@@ -242,35 +274,36 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     of ``x``; "mxfp8" / "mxfp4" an :class:`MxTensor` for :func:`gemm_mx`,
     quantised without rounding in between.  ``residual_out`` may be ``x`` or
     ``residual`` itself (updated in place)."""
-    _matrix(x, "x")
-    rows, cols = x.shape
-    dev, dtype = x.device, x.dtype
+    code, dtype, dev, shape = _dtype(x, "x"), x.dtype, x.device, x.shape
+    ldx = _matrix(x, "x", shape, dtype, dev)
+    rows, cols = shape
     fmt = 0 if format is None else _format(format)
-    _vector(weight, "weight", cols, dtype, dev)
+    w = _vector(weight, "weight", cols, dtype, dev)
+    h = r = None
+    ldr = ldh = 0
     if residual is not None:
-        _matrix(residual, "residual", (rows, cols), dtype, dev)
+        ldr = _matrix(residual, "residual", shape, dtype, dev)
+        r = residual.data_ptr()
+        if residual_out is None:
+            residual_out = _alloc(stream, dev, _new, rows, cols, dtype, dev)
+        ldh = _matrix(residual_out, "residual_out", shape, dtype, dev)
+        h = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    with _owner(stream, dev):
-        if out is None:
-            out = mx_empty(rows, cols, format, dev) if fmt else _new(rows, cols, dtype, dev)
-        if residual is not None and residual_out is None:
-            residual_out = _new(rows, cols, dtype, dev)
-    h = residual_out
-    if h is not None:
-        _matrix(h, "residual_out", (rows, cols), dtype, dev)
     if fmt:
-        _mx(out, "out", (rows, cols), format, dev)
-        y, s, ldy = out.data.data_ptr(), out.scales.data_ptr(), out._ld()
+        if out is None:
+            out = _alloc(stream, dev, mx_empty, rows, cols, format, dev)
+        else:
+            _mx_out(out, rows, cols, format, dev)
+        y, s, ldy = out.data.data_ptr(), out.scales.data_ptr(), out.ld
     else:
-        _matrix(out, "out", (rows, cols), dtype, dev)
-        y, s, ldy = out.data_ptr(), None, ops._ld_padded(out)
-    _call("mx_rms_norm", dev, stream, x.data_ptr(),
-          None if residual is None else residual.data_ptr(), weight.data_ptr(),
-          None if h is None else h.data_ptr(), y, s, rows, cols, ops._ld_padded(x),
-          0 if residual is None else ops._ld_padded(residual),
-          0 if h is None else ops._ld_padded(h), ldy, float(eps), _DTYPES[dtype], fmt)
-    return out if residual is None else (out, h)
+        if out is None:
+            out = _alloc(stream, dev, _new, rows, cols, dtype, dev)
+        ldy = _matrix(out, "out", shape, dtype, dev)
+        y, s = out.data_ptr(), None
+    _call("mx_rms_norm", dev, stream, x.data_ptr(), r, w, h, y, s, rows, cols, ldx, ldr, ldh, ldy,
+          eps, code, fmt)
+    return out if residual is None else (out, residual_out)
 
 
 def gemm_mx(a: MxTensor, b: MxTensor, bias: torch.Tensor | None = None, act: str | int = "none",
@@ -280,22 +313,21 @@ def gemm_mx(a: MxTensor, b: MxTensor, bias: torch.Tensor | None = None, act: str
     linear layer's weight, both MX of one format; ``bias`` N values of the
     output's type or None; ``act`` "none" / "relu" / "gelu".  C is fp16 or
     bf16 (``dtype``, or the type of ``out``); the sums are fp32."""
-    _mx(a, "a")
-    M, K = a.shape
-    _mx(b, "b", (b.rows, K) if isinstance(b, MxTensor) else None, a.format, a.device)
-    N, dev = b.rows, a.device
-    code = ops._ACTS[act] if isinstance(act, str) else int(act)
+    dev = _mx(a, "a")
+    if _mx(b, "b") != dev or b.cols != a.cols or b.format != a.format:
+        raise ValueError(f"a and b must share device, format and inner size: {a!r}, {b!r}")
+    M, N, K = a.rows, b.rows, a.cols
+    act = ops._ACTS[act] if isinstance(act, str) else int(act)
     if out is None:
         if dtype not in _DTYPES:
             raise TypeError("dtype must be torch.float16 or torch.bfloat16")
-        with _owner(stream, dev):
-            out = _new(M, N, dtype, dev)
-    _matrix(out, "out", (M, N), device=dev)
-    if bias is not None:
-        _vector(bias, "bias", N, out.dtype, dev)
+        out = _alloc(stream, dev, _new, M, N, dtype, dev)
+    code = _dtype(out, "out")
+    ldc = _matrix(out, "out", (M, N), out.dtype, dev)
+    bias = None if bias is None else _vector(bias, "bias", N, out.dtype, dev)
     _call("mx_gemm", dev, stream, a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(),
-          b.scales.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K,
-          a._ld(), b._ld(), ops._ld_padded(out), FORMATS[a.format], _DTYPES[out.dtype], code)
+          b.scales.data_ptr(), bias, out.data_ptr(), M, N, K, a.ld, b.ld, ldc, FORMATS[a.format],
+          code, act)
     return out
 
 
