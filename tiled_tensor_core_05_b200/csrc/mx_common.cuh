@@ -167,15 +167,21 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int64_t kt, int64_t til
   return ((r >> 7) * tiles + kt) * kTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
+// max(|a|, |b|, |c|); NaN (0x7FFFFFFF) if one is NaN.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
 // The MX form of 8 values of a row, a quarter of a block: called by all lanes
 // of a warp, 4 consecutive lanes holding the values of a block (missing ones
 // as 0).  Returns the block's scale byte; `q` receives the elements: 2 words
 // of E4M3 or 1 of E2M1.
 template <int FMT>
 __device__ __forceinline__ uint32_t quantize8(const float (&y)[8], uint32_t (&q)[2]) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+  uint32_t amax = __float_as_uint(max3_abs(max3_abs(max3_abs(y[0], y[1], y[2]), y[3], y[4]),
+                                           max3_abs(y[5], y[6], y[7]), 0.0f));
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   const uint32_t byte = scale_byte<FMT>(amax);

@@ -1,6 +1,8 @@
 // The row-wise MX operators: quantisation, its reverse, and the RMS norm with
 // the residual's addition and 16-bit or MX output.  All are bound by device
 // memory: each element is read once and written once.
+#include <type_traits>
+
 #include "mx_common.cuh"
 #include "mx_internal.h"
 
@@ -134,17 +136,20 @@ __global__ void __launch_bounds__(kTileThreads)
 // Precision: an MX element is decided by rounding at half steps, where the
 // last bits of y matter.  h^2 and h w are exact in fp32 (products of two
 // 16-bit values); the squares are summed with their rounding errors (two-sum)
-// and then in fp64; s is split into two fp32 numbers.  y is rounded to odd
-// (truncated, the last bit set when anything was cut off), which the rounding
-// to fewer bits that follows cannot tell from the exact value: every output
-// is the formula's value rounded once, up to about 2^-45 relative.  It costs
-// about ten packed instructions per element pair, hidden behind the loads.
+// and then in fp64; s is held as two fp32 numbers.  y in fp32 is on the same
+// side of every value halfway between two outputs as the exact y, unless it
+// lies on such a value itself, which its low bits show; only then is it
+// rounded to odd (truncated, the last bit set when anything was cut off),
+// which the rounding that follows cannot tell from the exact value.  So every
+// output is the formula's value rounded once, up to about 2^-43 relative, at
+// the price of two more instructions an element than a plain fp32 product.
 struct NormArgs {
   const uint16_t *X, *R, *W;
   uint16_t* H;
   void* Y;
   uint8_t* S;
   int64_t rows, cols, ldx, ldr, ldh, ldy;
+  double inv_cols;
   float eps;
 };
 
@@ -175,17 +180,45 @@ __device__ __forceinline__ float scale_odd(float p, float sh, float sl) {
   return a != 0.0f && fabsf(a) < __uint_as_float(0x7F800000u) ? __uint_as_float(b) : a;
 }
 
+// 16-bit additions, each rounded once.
 template <class T>
-__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
-  float x[8], y[8];
-  unpack8<T>(a, x);
-  unpack8<T>(b, y);
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b);
+template <>
+__device__ __forceinline__ uint4 add8<__half>(const uint4& a, const uint4& b) {
+  uint4 r;
 #pragma unroll
-  // rounding the fp32 sum again to 11 or 8 bits is the same as rounding once
-  // (24 >= 2 * 11 + 2)
-  for (int i = 0; i < 8; ++i) x[i] += y[i];
-  return pack8<T>(x);
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<__half2*>(&r)[i] = __hadd2_rn(reinterpret_cast<const __half2*>(&a)[i],
+                                                   reinterpret_cast<const __half2*>(&b)[i]);
+  return r;
 }
+template <>
+__device__ __forceinline__ uint4 add8<__nv_bfloat16>(const uint4& a, const uint4& b) {
+  uint4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<__nv_bfloat162*>(&r)[i] =
+        __hadd2_rn(reinterpret_cast<const __nv_bfloat162*>(&a)[i],
+                   reinterpret_cast<const __nv_bfloat162*>(&b)[i]);
+  return r;
+}
+
+// 1 / sqrt(v): the approximate instruction (2^-22) and one Newton step in
+// fp64 (2^-43); outside fp32's comfortable range, and for 0, inf and NaN, the
+// division.
+__device__ __forceinline__ double inverse_sqrt(double v) {
+  if (!(v > 1e-30 && v < 1e30)) return 1.0 / sqrt(v);
+  const double r = static_cast<double>(rsqrtf(static_cast<float>(v)));
+  return r * fma(-0.5 * v * r, r, 1.5);
+}
+
+// The low bits of an fp32 value that are all 0 halfway between two values of
+// the output type (and on them).
+template <class T, int FMT>
+constexpr uint32_t kTieMask = FMT == MX_FP8   ? 0x7FFFFu
+                              : FMT == MX_FP4 ? 0x1FFFFFu
+                              : std::is_same<T, __half>::value ? 0xFFFu
+                                                                                 : 0x7FFFu;
 
 template <class T, int FMT, int V>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
@@ -249,6 +282,19 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
       squares(u);
     }
   }
+  if constexpr (FMT != MX_NONE) {
+    // the rows that the last scale tile has no row for are cleared, their
+    // words dealt out over the threads of the rows that it has
+    const int64_t first = row & ~static_cast<int64_t>(kTileRows - 1);
+    const int64_t have = a.rows - first;
+    if (live && have < kTileRows) {
+      const uint32_t nt = static_cast<uint32_t>(tiles);
+      const uint32_t words = static_cast<uint32_t>(kTileRows - have) * nt;
+      for (uint32_t w = static_cast<uint32_t>(row - first) * tpr + threadIdx.x; w < words;
+           w += static_cast<uint32_t>(have) * tpr)
+        *reinterpret_cast<uint32_t*>(a.S + scale_word(first + have + w / nt, w % nt, tiles)) = 0;
+    }
+  }
   // an infinite sum has no rounding error (inf - inf is not one)
   double sum = (isinf(acc.x) || isinf(acc.y))
                    ? static_cast<double>(acc.x) + static_cast<double>(acc.y)
@@ -264,19 +310,37 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
     sum = 0.0;
     for (int w = 0; w < wpr; ++w) sum += mine[w];
   }
-  const double s = 1.0 / sqrt(sum / static_cast<double>(a.cols) + static_cast<double>(a.eps));
+  const double s = inverse_sqrt(fma(sum, a.inv_cols, static_cast<double>(a.eps)));
   const float sh = static_cast<float>(s);
   const float sl = static_cast<float>(s - static_cast<double>(sh));
 
   auto emit = [&](int64_t i, const uint4& u) {
     const int n = count(i);
-    float f[8], w[8];
-    unpack8<T>(u, f);
-    uint4 wv = make_uint4(0, 0, 0, 0);
-    if (n > 0) wv = load8(a.W + 8 * i, n);
-    unpack8<T>(wv, w);
+    float f[8];
+    {
+      uint4 wv = make_uint4(0, 0, 0, 0);
+      if (n > 0) wv = load8(a.W + 8 * i, n);
+      const uint32_t* hw = reinterpret_cast<const uint32_t*>(&u);
+      const uint32_t* ww = reinterpret_cast<const uint32_t*>(&wv);
+      float2 p[4];
+      uint32_t low = ~0u;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = n > 0 ? scale_odd(f[k] * w[k], sh, sl) : 0.0f;
+      for (int k = 0; k < 4; ++k) {
+        p[k] = __fmul2_rn(unpack2<T>(hw[k]), unpack2<T>(ww[k]));
+        const float2 y = __ffma2_rn(p[k], splat2(sh), __fmul2_rn(p[k], splat2(sl)));
+        low = min(low, min(__float_as_uint(y.x) & kTieMask<T, FMT>,
+                           __float_as_uint(y.y) & kTieMask<T, FMT>));
+        f[2 * k] = y.x;
+        f[2 * k + 1] = y.y;
+      }
+      if (low == 0u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[2 * k] = scale_odd(p[k].x, sh, sl);
+          f[2 * k + 1] = scale_odd(p[k].y, sh, sl);
+        }
+      }
+    }
     if (n < 8) {  // past the row's end: 0 whatever s is
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -314,23 +378,14 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
       emit(i, u);
     }
   }
-  if constexpr (FMT != MX_NONE) {
-    // the rows that the last scale tile has no row for: row k of the n that
-    // it has clears places k + n, k + 2n, ...
-    const int64_t first = row & ~static_cast<int64_t>(kTileRows - 1);
-    const int64_t have = a.rows - first;
-    if (live && have < kTileRows)
-      for (int64_t p = row + have; p < first + kTileRows; p += have)
-        for (int64_t kt = threadIdx.x; kt < tiles; kt += tpr)
-          *reinterpret_cast<uint32_t*>(a.S + scale_word(p, kt, tiles)) = 0;
-  }
 }
 
 template <class T, int FMT>
 int run_norm(const NormProblem& p) {
   const NormArgs a{static_cast<const uint16_t*>(p.X), static_cast<const uint16_t*>(p.R),
                    static_cast<const uint16_t*>(p.W), static_cast<uint16_t*>(p.H), p.Y,
-                   static_cast<uint8_t*>(p.S), p.rows, p.cols, p.ldx, p.ldr, p.ldh, p.ldy, p.eps};
+                   static_cast<uint8_t*>(p.S), p.rows, p.cols, p.ldx, p.ldr, p.ldh, p.ldy,
+                   1.0 / static_cast<double>(p.cols), p.eps};
   const int64_t vecs = 16 * scale_tiles(p.cols);  // vectors of a row, in whole scale tiles
   // two vectors a thread up to 512 threads, then four up to 1024; beyond 32768
   // columns a row is read twice (the second time mostly from L2)
