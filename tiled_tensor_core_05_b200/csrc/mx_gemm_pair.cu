@@ -9,14 +9,18 @@
 //     k-block, the scale tiles of its own rows of A, and those of all 256
 //     rows of B (each SM scales its half of the rows of D by all columns).
 //   * Per k-block the MMA thread copies the scale tiles of both SMs from
-//     shared memory to TMEM (tcgen05.cp), then issues 4 MMAs.  kSets sets of
-//     scale columns alternate; a set is overwritten only after the MMAs that
-//     read it have completed (the empty barrier of their ring stage).
+//     shared memory to TMEM (tcgen05.cp), then issues 4 MMAs.  Each ring stage
+//     has its own scale columns, so that a stage that may be filled again
+//     (its MMAs have completed) frees its columns too, and no other wait is
+//     needed.
 //   * TMEM holds 512 columns: two accumulators of 256 and the scales do not
 //     fit, so the accumulators share kOverlap columns: buffer 0 is columns
-//     0..255, buffer 1 ends where the scales begin.  The epilogue of a tile
-//     reads the shared columns first and hands them back at once, so the next
-//     tile's MMAs wait for one 64-column read instead of a whole epilogue.
+//     0..255, buffer 1 ends where the scales begin.  Every epilogue warp takes
+//     all its 64 columns into registers at once and then hands them back, so
+//     the next tile's MMAs wait for the reads of a tile, not for its epilogue.
+//   * 16 epilogue warps: the GELU epilogue is about 21 instructions and two
+//     special-function results an element, nearly as long as the MMAs of a
+//     4-bit tile with K = 4096; with 8 warps it was not hidden.
 #include "mx_internal.h"
 #include "mx_umma.cuh"
 #include "tile_common.cuh"
@@ -27,8 +31,10 @@ namespace {
 
 constexpr int kTile = 256;      // rows and columns of a pair's tile
 constexpr int kHalf = 128;      // rows of A and of B per CTA
-constexpr int kStages = 5;
-constexpr int kEpiWarps = 8;    // two per TMEM lane quarter, half of the columns each
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 16;   // four per TMEM lane quarter, 64 columns each
+constexpr int kWarpCols = 64;
+constexpr int kWarpRows = 32;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kPanelRows = 4096;  // rows of A per raster panel
 
@@ -38,14 +44,14 @@ struct PairCfg {
   static constexpr int kSf = Kind<FMT>::kSfTiles * kTileBytes;  // scales of 128 rows
   static constexpr int kStageBytes = 2 * kOperand + 3 * kSf;
   static constexpr int kBars = 2 * kStages + 6;
-  static constexpr int kSmemBytes =
-      1024 + kStages * kStageBytes + kEpiWarps * kEpiBuf + kBars * 8 + 16;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBars * 8 + 16;
   static constexpr int kSetCols = 3 * Kind<FMT>::kSfCols;  // scale columns of a k-block
-  static constexpr int kSets = 48 / kSetCols;
-  static constexpr int kSfBase = 512 - 48;
+  static constexpr int kSfBase = 512 - kStages * kSetCols;
   static constexpr int kAcc1 = kSfBase - kTile;  // first column of buffer 1
   static constexpr int kOverlap = kTile - kAcc1;
-  static_assert(kSets >= 2 && kOverlap <= kEpiCols, "TMEM columns");
+  // warps (of one CTA) that read a column both buffers share
+  static constexpr int kSharers = 4 * ((kOverlap + kWarpCols - 1) / kWarpCols);
+  static_assert(kAcc1 > 0, "TMEM columns");
   static_assert(kSmemBytes <= kMaxDynamicSmem, "shared memory budget");
 };
 
@@ -56,22 +62,54 @@ struct PairArgs {
   int M, N;
   int row_bytes, sf_tiles, num_kb;
   int group_m;
+  int wide;  // rows of C start on 32 bytes
   int* status;
   uint64_t timeout_ns;
 };
 
-// 64 fp32 accumulator columns of this thread's row -> 32 packed 16-bit pairs.
+// 32 aligned bytes, written once and not read again here.
+__device__ __forceinline__ void store_32(void* p, const uint32_t (&h)[8], uint64_t policy) {
+  asm volatile(
+      "st.global.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p),
+      "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]),
+      "l"(policy)
+      : "memory");
+}
+
+// The kWarpCols fp32 accumulators of this thread's row of C: bias, activation,
+// one rounding, stored 16 columns (a 32-byte sector) at a time straight from
+// registers.  Staging the tile in shared memory for TMA stores takes 32 KiB
+// from the operand ring and adds to the shared-memory traffic of the MMAs'
+// operands.
 template <class T, int ACT>
-__device__ __forceinline__ void convert(const uint32_t (&v)[64], const uint16_t* bias, int col0,
-                                        int N, uint32_t (&h)[32]) {
-  uint32_t bb[32];
-  if (bias != nullptr) load_bias_chunk(reinterpret_cast<const __half*>(bias), col0, N, bb);
+__device__ __forceinline__ void store_columns(const uint32_t (&v)[kWarpCols], const PairArgs& a,
+                                              int row, int col0, uint64_t policy) {
+  uint16_t* c = a.C + static_cast<int64_t>(row) * a.ldc + col0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-    if (bias != nullptr) x = __fadd2_rn(x, unpack2<T>(bb[i]));
-    x = activate2<ACT>(x);
-    h[i] = pack2<T>(x.x, x.y);
+  for (int i = 0; i < kWarpCols; i += 16) {
+    const int n = a.N - (col0 + i);
+    if (n <= 0) break;
+    uint4 b[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (a.bias != nullptr) {
+      b[0] = load8(a.bias + col0 + i, n);
+      if (n > 8) b[1] = load8(a.bias + col0 + i + 8, n - 8);
+    }
+    const uint32_t* bw = reinterpret_cast<const uint32_t*>(b);
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float2 x = make_float2(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+      if (a.bias != nullptr) x = __fadd2_rn(x, unpack2<T>(bw[k]));
+      x = activate2<ACT>(x);
+      h[k] = pack2<T>(x.x, x.y);
+    }
+    if (row >= a.M) continue;
+    if (n >= 16 && a.wide) {
+      store_32(c + i, h, policy);
+    } else {
+      store8(c + i, make_uint4(h[0], h[1], h[2], h[3]), n);
+      if (n > 8) store8(c + i + 8, make_uint4(h[4], h[5], h[6], h[7]), n - 8);
+    }
   }
 }
 
@@ -80,15 +118,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     pair_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSA,
-                     const __grid_constant__ CUtensorMap tmSB,
-                     const __grid_constant__ CUtensorMap tmC, const PairArgs a) {
+                     const __grid_constant__ CUtensorMap tmSB, const PairArgs a) {
   using Cfg = PairCfg<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* smA = smem;
   uint8_t* smB = smA + kStages * Cfg::kOperand;
-  uint8_t* smEpi = smB + kStages * Cfg::kOperand;
-  uint8_t* smS = smEpi + kEpiWarps * kEpiBuf;  // per stage: scales of A, of B's two halves
+  uint8_t* smS = smB + kStages * Cfg::kOperand;  // per stage: scales of A, of B's two halves
   uint64_t* full = reinterpret_cast<uint64_t*>(smS + kStages * 3 * Cfg::kSf);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;   // [2]
@@ -107,7 +143,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int num_m = (a.M + kTile - 1) / kTile;
   const int num_n = (a.N + kTile - 1) / kTile;
   const int num_tiles = num_m * num_n;
-  const int n8 = a.N & ~7;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -118,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * kEpiWarps);
     }
-    mbar_init(shared_empty, kEpiWarps);
+    mbar_init(shared_empty, 2 * Cfg::kSharers);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -126,7 +161,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
-    tma_prefetch_desc(&tmC);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -194,11 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer (leader) ---
     if (leader && lane == 0) {
-      int stage = 0, old_stage = 0;  // ring stage of this k-block, and of the one kSets before
-      uint32_t phase = 0, old_phase = 0, down = 0;
-      int buf = 0, set = 0;
+      int stage = 0;
+      uint32_t phase = 0, down = 0;
+      int buf = 0;
       uint32_t acc_phase = 0, shared_phase = 0;
-      int64_t issued = 0;  // k-blocks so far
       bool ok = true;
       int site = 0;
       for (int tile = pair; tile < num_tiles && ok; tile += npairs, down ^= 1u) {
@@ -224,24 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             site = 6;
             break;
           }
-          if (issued >= Cfg::kSets) {  // the MMAs that read this set of scales are done
-            if (!mbar_wait(&empty[old_stage], old_phase, abort_flag, a.timeout_ns)) {
-              ok = false;
-              site = 8;
-              break;
-            }
-            if (++old_stage == kStages) {
-              old_stage = 0;
-              old_phase ^= 1u;
-            }
-          }
-          ++issued;
           tc_fence_after_sync();
           const uint32_t a_addr = smem_u32(smA + stage * Cfg::kOperand);
           const uint32_t b_addr = smem_u32(smB + stage * Cfg::kOperand);
           const uint32_t s_addr = smem_u32(smS + stage * 3 * Cfg::kSf);
           // columns: 4 per tile of A's scales, then 8 per tile of B's (256 rows)
-          const uint32_t sfa = tmem + Cfg::kSfBase + static_cast<uint32_t>(set * Cfg::kSetCols);
+          const uint32_t sfa = tmem + Cfg::kSfBase + static_cast<uint32_t>(stage * Cfg::kSetCols);
           const uint32_t sfb = sfa + Kind<FMT>::kSfCols;
 #pragma unroll
           for (int t = 0; t < Kind<FMT>::kSfTiles; ++t) {
@@ -260,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                            (i | k) != 0 ? 1u : 0u);
           }
           umma_commit_pair(&empty[stage], 0x3);  // stage free in both CTAs
-          if (++set == Cfg::kSets) set = 0;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
@@ -281,10 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ epilogue (both CTAs) ---
     const int q = warp & 3;
     const int ew = warp - 2;
-    const int g = ew >> 2;  // columns 128 g .. 128 g + 127 of the tile
-    uint8_t* box = smEpi + ew * kEpiBuf;
+    const int g = ew >> 2;  // columns 64 g .. 64 g + 63 of the tile
+    const uint64_t policy = l2_policy_evict_first();
     int buf = 0;
-    uint32_t acc_phase = 0, chunk_no = 0;
+    uint32_t acc_phase = 0;
     for (int tile = pair; tile < num_tiles; tile += npairs) {
       int mb, nb;
       tile_coords(tile, num_m, num_n, a.group_m, mb, nb);
@@ -297,32 +317,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after_sync();
-      const int row0 = mb * kTile + rank * kHalf + q * kEpiRows;
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                             static_cast<uint32_t>(buf ? Cfg::kAcc1 : 0);
-      // shared columns: the last ones of buffer 0, the first ones of buffer 1
-      const int first = buf == 0 && g == 1 ? 1 : 0;
-      const bool has_shared = g == (buf ^ 1);
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        const int col = (2 * g + (c ^ first)) * kEpiCols;
-        uint32_t v[64], h[32];
-        tmem_load_32x32b_x64(t_row + col, v);
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (c == 0 && has_shared) mbar_arrive_cluster_relaxed(shared_empty_leader);
-          if (c == 1) mbar_arrive_cluster_relaxed(acc_empty_leader + buf * 8);
-        }
-        convert<T, ACT>(v, a.bias, nb * kTile + col, a.N, h);
-        stage_chunk<1>(h, box, chunk_no, &tmC, reinterpret_cast<__half*>(a.C), a.ldc, a.M, a.N, n8,
-                       row0, nb * kTile + col, lane);
+      const int row0 = mb * kTile + rank * kHalf + q * kWarpRows;
+      const int col0 = nb * kTile + g * kWarpCols;
+      uint32_t v[kWarpCols];
+      tmem_load_32x32b_x64(tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                               static_cast<uint32_t>((buf ? Cfg::kAcc1 : 0) + g * kWarpCols),
+                           v);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        // the columns both buffers share: the last ones of buffer 0, the first of buffer 1
+        const bool shares = buf == 0 ? (g + 1) * kWarpCols > Cfg::kAcc1
+                                     : g * kWarpCols < Cfg::kOverlap;
+        if (shares) mbar_arrive_cluster_relaxed(shared_empty_leader);
+        mbar_arrive_cluster_relaxed(acc_empty_leader + buf * 8);
       }
+      store_columns<T, ACT>(v, a, row0 + lane, col0, policy);
       buf ^= 1;
       if (buf == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) bulk_wait_group<0>();
-    __syncwarp();
   }
 
   tc_fence_before_sync();
@@ -346,15 +359,12 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
     return GEMM_ERR_LAUNCH;
   const int64_t row_bytes = mx_row_bytes(p.K, FMT);
   const int64_t sf_tiles = scale_tiles(p.K);
-  const uint64_t n8 = static_cast<uint64_t>(p.N) & ~7ull;
   constexpr int kBox = Kind<FMT>::kSfTiles;
-  CUtensorMap tA, tB, tSA, tSB, tC;
+  CUtensorMap tA, tB, tSA, tSB;
   int rc = encode_tmap_u8_2d(&tA, p.A, row_bytes, p.M, p.lda, kHalf);
   if (rc == 0) rc = encode_tmap_u8_2d(&tB, p.B, row_bytes, p.N, p.ldb, kHalf);
   if (rc == 0) rc = encode_tmap_scales(&tSA, p.SA, (p.M + 127) / 128 * sf_tiles, kBox);
   if (rc == 0) rc = encode_tmap_scales(&tSB, p.SB, (p.N + 127) / 128 * sf_tiles, kBox);
-  // (the map of C is never used when n8 is 0)
-  if (rc == 0) rc = encode_tmap_f16_2d(&tC, p.C, n8 > 0 ? n8 : 8, p.M, p.ldc, kEpiCols, kEpiRows);
   if (rc != 0) return rc;
   Launch l(dim3(2 * (d.sm_count / 2)), dim3(kThreads), Cfg::kSmemBytes, p.stream);
   l.cluster(2);
@@ -378,9 +388,10 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
                    static_cast<int>(sf_tiles),
                    static_cast<int>((row_bytes + kRowBytes - 1) / kRowBytes),
                    group_tiles(kPanelRows, kTile, kTile),
+                   (reinterpret_cast<uintptr_t>(p.C) & 31) == 0 && p.ldc % 16 == 0,
                    d.status,
                    d.timeout_ns};
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tA, tB, tSA, tSB, tC, a);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tA, tB, tSA, tSB, a);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
