@@ -131,7 +131,10 @@ __global__ void __launch_bounds__(kTileThreads)
 //
 // blockDim.x threads share a row, each with the 16-byte vectors threadIdx.x +
 // v blockDim.x of it (V of them in registers; V = 0 reads h twice), so that 4
-// consecutive lanes hold a block of 32.
+// consecutive lanes hold a block of 32.  What a thread does once for a row
+// (sums across lanes and warps, the square root, addresses: some 250
+// instructions) is shared by 8 V elements, so many rows take V = 4 and few
+// threads each; few rows take more threads with fewer vectors, for latency.
 //
 // Precision: an MX element is decided by rounding at half steps, where the
 // last bits of y matter.  h^2 and h w are exact in fp32 (products of two
@@ -143,6 +146,8 @@ __global__ void __launch_bounds__(kTileThreads)
 // which the rounding that follows cannot tell from the exact value.  So every
 // output is the formula's value rounded once, up to about 2^-43 relative, at
 // the price of two more instructions an element than a plain fp32 product.
+constexpr int64_t kSms = 148;  // of a B200, to choose V
+
 struct NormArgs {
   const uint16_t *X, *R, *W;
   uint16_t* H;
@@ -220,26 +225,39 @@ constexpr uint32_t kTieMask = FMT == MX_FP8   ? 0x7FFFFu
                               : std::is_same<T, __half>::value ? 0xFFFu
                                                                                  : 0x7FFFu;
 
+template <int V>
+constexpr int kNormThreads = V >= 4 ? 512 : 1024;
+
 template <class T, int FMT, int V>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArgs a) {
   __shared__ double part[32];
   const int tpr = blockDim.x;
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool live = row < a.rows;
-  const int64_t tiles = scale_tiles(a.cols);
+  const int cols = static_cast<int>(a.cols);
+  const int whole = live ? cols >> 3 : 0;  // vectors of 8 elements; then `tail` elements
+  const int tail = live ? cols & 7 : 0;
+  const int tiles = static_cast<int>(scale_tiles(a.cols));
   // vectors a thread walks over: all of the row's 128-column tiles
-  const int steps = V > 0 ? V : static_cast<int>((16 * tiles + tpr - 1) / tpr);
-  const uint16_t* x = a.X + row * a.ldx;
-  const uint16_t* r = a.R != nullptr ? a.R + row * a.ldr : nullptr;
-  uint16_t* h = a.H != nullptr ? a.H + row * a.ldh : nullptr;
-  auto count = [&](int64_t i) {
-    const int64_t left = live ? a.cols - 8 * i : 0;
-    return left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left));
+  const int steps = V > 0 ? V : (16 * tiles + tpr - 1) / tpr;
+  auto load = [&](const uint16_t* p, int i) {
+    if (i < whole) return *reinterpret_cast<const uint4*>(p + 8 * static_cast<int64_t>(i));
+    if (i == whole && tail != 0) return load8(p + 8 * static_cast<int64_t>(i), tail);
+    return make_uint4(0, 0, 0, 0);
+  };
+  auto store = [&](uint16_t* p, int i, const uint4& v) {
+    if (i < whole)
+      *reinterpret_cast<uint4*>(p + 8 * static_cast<int64_t>(i)) = v;
+    else if (i == whole && tail != 0)
+      store8(p + 8 * static_cast<int64_t>(i), v, tail);
   };
   grid_dependency_trigger();
   grid_dependency_wait();
 
+  const uint16_t* x = a.X + row * a.ldx;
+  const uint16_t* r = a.R != nullptr ? a.R + row * a.ldr : nullptr;
+  uint16_t* h = a.H != nullptr ? a.H + row * a.ldh : nullptr;
   uint4 hv[V > 0 ? V : 1];
   float2 acc = make_float2(0.0f, 0.0f), err = make_float2(0.0f, 0.0f);
   auto squares = [&](const uint4& v) {
@@ -248,36 +266,27 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
     for (int k = 0; k < 4; ++k) add_square(acc, err, unpack2<T>(w[k]));
   };
   if constexpr (V > 0) {
-    uint4 rv[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
-      const int n = count(i);
-      hv[v] = rv[v] = make_uint4(0, 0, 0, 0);
-      if (n > 0) {
-        hv[v] = load8(x + 8 * i, n);
-        if (r != nullptr) rv[v] = load8(r + 8 * i, n);
-      }
-    }
+    for (int v = 0; v < V; ++v) hv[v] = load(x, threadIdx.x + v * tpr);
+    if (r != nullptr) {
+      uint4 rv[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (r != nullptr) {
-        const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
-        const int n = count(i);
+      for (int v = 0; v < V; ++v) rv[v] = load(r, threadIdx.x + v * tpr);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         hv[v] = add8<T>(hv[v], rv[v]);
-        if (h != nullptr && n > 0) store8(h + 8 * i, hv[v], n);
+        if (h != nullptr) store(h, threadIdx.x + v * tpr, hv[v]);
       }
-      squares(hv[v]);
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) squares(hv[v]);
   } else {
     for (int v = 0; v < steps; ++v) {
-      const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
-      const int n = count(i);
-      if (n == 0) continue;
-      uint4 u = load8(x + 8 * i, n);
+      const int i = threadIdx.x + v * tpr;
+      uint4 u = load(x, i);
       if (r != nullptr) {
-        u = add8<T>(u, load8(r + 8 * i, n));
-        if (h != nullptr) store8(h + 8 * i, u, n);
+        u = add8<T>(u, load(r, i));
+        if (h != nullptr) store(h, i, u);
       }
       squares(u);
     }
@@ -314,43 +323,40 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
   const float sh = static_cast<float>(s);
   const float sl = static_cast<float>(s - static_cast<double>(sh));
 
-  auto emit = [&](int64_t i, const uint4& u) {
-    const int n = count(i);
+  auto emit = [&](int i, const uint4& u) {
+    const uint4 wv = load(a.W, i);
+    const uint32_t* hw = reinterpret_cast<const uint32_t*>(&u);
+    const uint32_t* ww = reinterpret_cast<const uint32_t*>(&wv);
     float f[8];
-    {
-      uint4 wv = make_uint4(0, 0, 0, 0);
-      if (n > 0) wv = load8(a.W + 8 * i, n);
-      const uint32_t* hw = reinterpret_cast<const uint32_t*>(&u);
-      const uint32_t* ww = reinterpret_cast<const uint32_t*>(&wv);
-      float2 p[4];
-      uint32_t low = ~0u;
+    float2 p[4];
+    uint32_t low = ~0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      p[k] = __fmul2_rn(unpack2<T>(hw[k]), unpack2<T>(ww[k]));
+      const float2 y = __ffma2_rn(p[k], splat2(sh), __fmul2_rn(p[k], splat2(sl)));
+      low = min(low, min(__float_as_uint(y.x) & kTieMask<T, FMT>,
+                         __float_as_uint(y.y) & kTieMask<T, FMT>));
+      f[2 * k] = y.x;
+      f[2 * k + 1] = y.y;
+    }
+    if (low == 0u) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        p[k] = __fmul2_rn(unpack2<T>(hw[k]), unpack2<T>(ww[k]));
-        const float2 y = __ffma2_rn(p[k], splat2(sh), __fmul2_rn(p[k], splat2(sl)));
-        low = min(low, min(__float_as_uint(y.x) & kTieMask<T, FMT>,
-                           __float_as_uint(y.y) & kTieMask<T, FMT>));
-        f[2 * k] = y.x;
-        f[2 * k + 1] = y.y;
+        f[2 * k] = scale_odd(p[k].x, sh, sl);
+        f[2 * k + 1] = scale_odd(p[k].y, sh, sl);
       }
-      if (low == 0u) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[2 * k] = scale_odd(p[k].x, sh, sl);
-          f[2 * k + 1] = scale_odd(p[k].y, sh, sl);
-        }
-      }
-    }
-    if (n < 8) {  // past the row's end: 0 whatever s is
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k >= n) f[k] = 0.0f;
     }
     if constexpr (FMT == MX_NONE) {
-      if (n > 0) store8(static_cast<uint16_t*>(a.Y) + row * a.ldy + 8 * i, pack8<T>(f), n);
+      store(static_cast<uint16_t*>(a.Y) + row * a.ldy, i, pack8<T>(f));
     } else {
+      if (i >= whole) {  // past the row's end: 0 whatever s is
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i > whole || k >= tail) f[k] = 0.0f;
+      }
       uint32_t q[2];
       uint32_t word = quantize8<FMT>(f, q) << (8 * ((lane >> 2) & 3));
+      const int n = i < whole ? 8 : (i == whole ? tail : 0);
       if (n > 0) store_elements<FMT>(static_cast<uint8_t*>(a.Y) + row * a.ldy, i, q, n);
       // the 4 blocks of a 128-column tile are 16 lanes: their bytes make a word
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
@@ -361,23 +367,29 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
   };
   if constexpr (V > 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) emit(threadIdx.x + static_cast<int64_t>(v) * tpr, hv[v]);
+    for (int v = 0; v < V; ++v) emit(threadIdx.x + v * tpr, hv[v]);
   } else {
     for (int v = 0; v < steps; ++v) {
-      const int64_t i = threadIdx.x + static_cast<int64_t>(v) * tpr;
-      const int n = count(i);
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (n > 0) {
-        if (r != nullptr && h != nullptr) {
-          u = load8(h + 8 * i, n);  // written by this thread above
-        } else {
-          u = load8(x + 8 * i, n);
-          if (r != nullptr) u = add8<T>(u, load8(r + 8 * i, n));
-        }
+      const int i = threadIdx.x + v * tpr;
+      uint4 u;
+      if (r != nullptr && h != nullptr) {
+        u = load(h, i);  // written by this thread above
+      } else {
+        u = load(x, i);
+        if (r != nullptr) u = add8<T>(u, load(r, i));
       }
       emit(i, u);
     }
   }
+}
+
+template <class T, int FMT, int V>
+cudaError_t launch_norm(const NormProblem& p, const NormArgs& a, int threads) {
+  // rows of one warp go several to a CTA
+  const int64_t per_cta = threads == 32 ? (p.rows < 4 ? p.rows : 4) : 1;
+  Launch l(dim3(static_cast<unsigned>((p.rows + per_cta - 1) / per_cta)),
+           dim3(static_cast<unsigned>(threads), static_cast<unsigned>(per_cta)), 0, p.stream);
+  return cudaLaunchKernelEx(&l.cfg, rms_norm_kernel<T, FMT, V>, a);
 }
 
 template <class T, int FMT>
@@ -386,24 +398,23 @@ int run_norm(const NormProblem& p) {
                    static_cast<const uint16_t*>(p.W), static_cast<uint16_t*>(p.H), p.Y,
                    static_cast<uint8_t*>(p.S), p.rows, p.cols, p.ldx, p.ldr, p.ldh, p.ldy,
                    1.0 / static_cast<double>(p.cols), p.eps};
-  const int64_t vecs = 16 * scale_tiles(p.cols);  // vectors of a row, in whole scale tiles
-  // two vectors a thread up to 512 threads, then four up to 1024; beyond 32768
-  // columns a row is read twice (the second time mostly from L2)
-  int tpr = 32;
-  while (tpr < 512 && 2 * tpr < vecs) tpr *= 2;
-  if (2 * tpr < vecs) tpr = 1024;
-  const int per_cta = tpr < 256 ? 256 / tpr : 1;
-  const int rows_per_cta = static_cast<int>(p.rows < per_cta ? p.rows : per_cta);
-  const int64_t grid = (p.rows + rows_per_cta - 1) / rows_per_cta;
-  Launch l(dim3(static_cast<unsigned>(grid)),
-           dim3(static_cast<unsigned>(tpr), static_cast<unsigned>(rows_per_cta)), 0, p.stream);
+  // vectors of a row, in whole scale tiles; V as large as leaves 1024 threads
+  // an SM, and at least what the largest CTA needs
+  const int64_t vecs = 16 * scale_tiles(p.cols);
+  const auto threads = [&](int v) { return (vecs + 32 * v - 1) / (32 * v) * 32; };
+  int v = 4;
+  while (v > 1 && p.rows * threads(v) < 1024 * kSms && threads(v / 2) <= (v / 2 >= 4 ? 512 : 1024))
+    v /= 2;
+  const int64_t t = threads(v);
   cudaError_t e;
-  if (vecs <= 2 * tpr)
-    e = cudaLaunchKernelEx(&l.cfg, rms_norm_kernel<T, FMT, 2>, a);
-  else if (vecs <= 4 * tpr)
-    e = cudaLaunchKernelEx(&l.cfg, rms_norm_kernel<T, FMT, 4>, a);
+  if (t > (v >= 4 ? 512 : 1024))  // beyond 16384 columns
+    e = launch_norm<T, FMT, 0>(p, a, 1024);
+  else if (v == 4)
+    e = launch_norm<T, FMT, 4>(p, a, static_cast<int>(t));
+  else if (v == 2)
+    e = launch_norm<T, FMT, 2>(p, a, static_cast<int>(t));
   else
-    e = cudaLaunchKernelEx(&l.cfg, rms_norm_kernel<T, FMT, 0>, a);
+    e = launch_norm<T, FMT, 1>(p, a, static_cast<int>(t));
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
