@@ -28,9 +28,15 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kTileN = 128;  // columns of C per tile
 
-template <int FMT, int BN>
+// Ring depths: kDeep stages leave room for two CTAs an SM (one for BN = 128:
+// two with 3 stages), 3 stages for three.
+constexpr int kShallow = 3;
+constexpr int kDeep = 5;
+constexpr int deep_stages(int bn) { return bn == 128 ? 3 : bn == 64 ? 4 : kDeep; }
+
+template <int FMT, int BN, int STAGES>
 struct SplitCfg {
-  static constexpr int kStages = BN == 64 ? 4 : 3;
+  static constexpr int kStages = STAGES;
   static constexpr int kWBytes = kTileN * kRowBytes;
   static constexpr int kXBytes = BN * kRowBytes;
   static constexpr int kSfBytes = Kind<FMT>::kSfTiles * kTileBytes;
@@ -43,6 +49,11 @@ struct SplitCfg {
   static constexpr int kSfBase = BN < 32 ? 32 : BN;
   static constexpr int kCols = kSfBase + kStages * 2 * Kind<FMT>::kSfCols;
   static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+  // CTAs an SM holds at once (228 KiB of shared memory, 1 KiB of it per CTA
+  // the system's; 512 TMEM columns)
+  static constexpr int kPerSm = 228 * 1024 / (kSmemBytes + 1024) < 512 / static_cast<int>(kTmemCols)
+                                    ? 228 * 1024 / (kSmemBytes + 1024)
+                                    : 512 / static_cast<int>(kTmemCols);
   static_assert(kCols <= 256, "TMEM columns");
   static_assert(kSmemBytes <= kMaxDynamicSmem, "shared memory budget");
 };
@@ -57,6 +68,7 @@ struct SplitArgs {
   int tiles;      // scale tiles along K
   int stages;     // ring stages along K
   int tiles_m;
+  int stream_b;   // B is read once: let L2 drop it first
   int dtype, act;
   int* status;
   uint64_t timeout_ns;
@@ -95,12 +107,12 @@ __device__ __forceinline__ void store_row8(const SplitArgs& a, int m, int n, con
   store8(a.C + static_cast<int64_t>(m) * a.ldc + n, pack8<T>(y), count);
 }
 
-template <int FMT, int BN>
+template <int FMT, int BN, int STAGES>
 __global__ void __launch_bounds__(kThreads)
     split_gemm_kernel(const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmA, const SplitArgs a) {
-  using Cfg = SplitCfg<FMT, BN>;
-  constexpr int kStages = Cfg::kStages;
+  using Cfg = SplitCfg<FMT, BN, STAGES>;
+  constexpr int kStages = STAGES;
   constexpr int kSfTiles = Kind<FMT>::kSfTiles;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -153,6 +165,7 @@ __global__ void __launch_bounds__(kThreads)
       int stage = 0;
       uint32_t phase = 0, armed = 0, parity = 0;
       bool ok = true;
+      const uint64_t policy = l2_policy_evict_first();
       for (int s = s_begin; s < s_end; ++s) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns)) {
           ok = false;
@@ -162,7 +175,11 @@ __global__ void __launch_bounds__(kThreads)
         const int kt = s * kSfTiles;
         const uint32_t sf = static_cast<uint32_t>(min(kSfTiles, a.tiles - kt)) * kTileBytes;
         mbar_arrive_expect_tx(&full[stage], Cfg::kWBytes + Cfg::kXBytes + 2 * sf);
-        tma_load_2d(&tmB, &full[stage], smW + stage * Cfg::kWBytes, s * kRowBytes, n0);
+        uint8_t* w = smW + stage * Cfg::kWBytes;
+        if (a.stream_b)
+          tma_load_2d_hint(&tmB, &full[stage], w, s * kRowBytes, n0, policy);
+        else
+          tma_load_2d(&tmB, &full[stage], w, s * kRowBytes, n0);
         tma_load_2d(&tmA, &full[stage], smX + stage * Cfg::kXBytes, s * kRowBytes, m0);
         uint8_t* sfw = smS + stage * 2 * Cfg::kSfBytes;
         bulk_load(sfw, a.SB + (static_cast<int64_t>(nt) * a.tiles + kt) * kTileBytes, sf,
@@ -200,6 +217,8 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t s_addr = smem_u32(smS + stage * 2 * Cfg::kSfBytes);
         const uint32_t sfw = tmem + Cfg::kSfBase + stage * 2 * Kind<FMT>::kSfCols;
         const uint32_t sfx = sfw + Kind<FMT>::kSfCols;
+        // rows 64 .. 127 of a scale tile are its columns 2 and 3
+        const uint32_t half = BN == 64 ? static_cast<uint32_t>(mt & 1) * 2u : 0u;
         const int have = min(kSfTiles, a.tiles - s * kSfTiles);
 #pragma unroll
         for (int t = 0; t < kSfTiles; ++t) {
@@ -215,7 +234,7 @@ __global__ void __launch_bounds__(kThreads)
           const int t = FMT == MX_FP8 ? 0 : k / 2;
           mx_mma<FMT, 1>(tmem, smem_desc_sw128(w_addr + k * kMmaBytes, 16, 1024),
                          smem_desc_sw128(x_addr + k * kMmaBytes, 16, 1024),
-                         mx_idesc<FMT>(kTileN, BN, k), sfw + 4 * t, sfx + 4 * t,
+                         mx_idesc<FMT>(kTileN, BN, k), sfw + 4 * t, sfx + 4 * t + half,
                          (s != s_begin || k != 0) ? 1u : 0u);
         }
         umma_commit(&empty[stage]);
@@ -294,19 +313,69 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <int FMT, int BN>
-int launch(const MxGemmProblem& p, const DeviceCtx& d) {
-  using Cfg = SplitCfg<FMT, BN>;
+// Clusters of c = 1 .. 8 CTAs that the GPU holds at one CTA an SM (0 = not
+// asked yet, per device; the GPCs leave SMs over).
+struct Residency {
+  std::atomic<int> clusters[9] = {};
+};
+
+// Into how many parts of at least two k-blocks K is divided: as many as run in
+// one wave, since a second wave costs more than the division brings
+// (14336 x 4096 MXFP8 for one token: 12.5 us as 3 x 112 CTAs, 17.7 as 4 x 112).
+// Larger clusters take a place an SM only, where they find it sooner and the
+// joining of many parts costs as much as it saves (16 x 4096 x 8192 MXFP4, 32
+// tiles: 4 parts 8.5 us, 5 parts 9.0, 8 parts 9.1; 60 x 8192 x 4096, 64 tiles
+// of 64 rows: 2 parts 10.0 us, 3 parts 11.6).
+template <int FMT, int BN, int STAGES>
+int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
+  using Cfg = SplitCfg<FMT, BN, STAGES>;
+  static Residency residency[64];
+  int splits = 1;
+  for (int c = 2; c <= 8 && stages >= 2 * c; ++c) {
+    std::atomic<int>& known = residency[d.device & 63].clusters[c];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+      Launch l(dim3(static_cast<unsigned>(c * d.sm_count)), dim3(kThreads), Cfg::kSmemBytes,
+               nullptr);
+      l.cluster(static_cast<unsigned>(c));
+      if (cudaOccupancyMaxActiveClusters(&n, split_gemm_kernel<FMT, BN, STAGES>, &l.cfg) !=
+              cudaSuccess ||
+          n <= 0) {
+        cudaGetLastError();
+        n = d.sm_count / (c + 1);
+      }
+      known.store(n, std::memory_order_relaxed);
+    }
+    const bool dense = c == 2 || (c == 3 && BN <= 32);
+    if (tiles <= static_cast<int64_t>(n) * (dense ? Cfg::kPerSm : 1)) splits = c;
+  }
+  return splits;
+}
+
+template <int FMT, int BN, int STAGES>
+bool set_attributes(const DeviceCtx& d) {
   static std::atomic<uint64_t> attr_done{0};
-  auto kern = split_gemm_kernel<FMT, BN>;
+  auto kern = split_gemm_kernel<FMT, BN, STAGES>;
+  using Cfg = SplitCfg<FMT, BN, STAGES>;
   const uint64_t bit = 1ull << (d.device & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg::kSmemBytes) != cudaSuccess)
-      return GEMM_ERR_LAUNCH;
+                             Cfg::kSmemBytes) != cudaSuccess ||
+        // several CTAs an SM: all of the SM's memory as shared memory
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+      return false;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
+  return true;
+}
+
+template <int FMT, int BN, int STAGES>
+int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
+  using Cfg = SplitCfg<FMT, BN, STAGES>;
+  auto kern = split_gemm_kernel<FMT, BN, STAGES>;
   const int64_t row_bytes = mx_row_bytes(p.K, FMT);
   CUtensorMap tB, tA;
   int rc = encode_tmap_u8_2d(&tB, p.B, row_bytes, p.N, p.ldb, kTileN);
@@ -315,9 +384,6 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
   const int64_t stages = (row_bytes + kRowBytes - 1) / kRowBytes;
   const int64_t tiles_m = (p.M + BN - 1) / BN;
   const int64_t tiles = tiles_m * ((p.N + kTileN - 1) / kTileN);
-  const int resident = d.sm_count * (kMaxDynamicSmem / Cfg::kSmemBytes);
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= resident && stages >= splits * 4) splits *= 2;
   if (tiles * splits > INT32_MAX) return GEMM_ERR_INVALID_ARG;
   const SplitArgs a{static_cast<const uint8_t*>(p.SB),
                     static_cast<const uint8_t*>(p.SA),
@@ -330,6 +396,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
                     static_cast<int>(scale_tiles(p.K)),
                     static_cast<int>(stages),
                     static_cast<int>(tiles_m),
+                    tiles_m == 1,
                     p.dtype,
                     p.act,
                     d.status,
@@ -340,12 +407,32 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
+// Up to 16 rows: three CTAs an SM where that divides K further than two of a
+// deeper ring (12.5 us instead of 13.4 above); else the deeper ring (32 x
+// 28672 x 8192 MXFP4: 22.6 us instead of 24.4).
+template <int FMT, int BN>
+int launch_depth(const MxGemmProblem& p, const DeviceCtx& d) {
+  constexpr int kStages = deep_stages(BN);
+  if (!set_attributes<FMT, BN, kStages>(d)) return GEMM_ERR_LAUNCH;
+  const int64_t tiles = (p.M + BN - 1) / BN * ((p.N + kTileN - 1) / kTileN);
+  const int64_t stages = (mx_row_bytes(p.K, FMT) + kRowBytes - 1) / kRowBytes;
+  const int deep = choose_splits<FMT, BN, kStages>(tiles, stages, d);
+  if constexpr (BN == 16) {
+    if (!set_attributes<FMT, BN, kShallow>(d)) return GEMM_ERR_LAUNCH;
+    const int shallow = choose_splits<FMT, BN, kShallow>(tiles, stages, d);
+    if (shallow > deep) return launch<FMT, BN, kShallow>(p, d, shallow);
+  }
+  return launch<FMT, BN, kStages>(p, d, deep);
+}
+
 template <int FMT>
 int launch_rows(const MxGemmProblem& p, const DeviceCtx& d) {
-  if (p.M <= 16) return launch<FMT, 16>(p, d);
-  if (p.M <= 32) return launch<FMT, 32>(p, d);
-  if (p.M <= 64) return launch<FMT, 64>(p, d);
-  return launch<FMT, 128>(p, d);
+  if (p.M <= 16) return launch_depth<FMT, 16>(p, d);
+  if (p.M <= 32) return launch_depth<FMT, 32>(p, d);
+  // 64 rows a tile as long as 128 would leave most SMs without one
+  const int64_t tiles128 = (p.M + 127) / 128 * ((p.N + 127) / 128);
+  if (p.M <= 64 || tiles128 < d.sm_count / 2) return launch_depth<FMT, 64>(p, d);
+  return launch_depth<FMT, 128>(p, d);
 }
 
 template <class T>
