@@ -39,10 +39,9 @@ _MX = __all__[__all__.index("MxTensor"):]
 
 
 def __getattr__(name):
-    if name in _MX:
-        from . import mx
-        return getattr(mx, name)
     if name in __all__:
-        from . import ops
-        return getattr(ops, name)
+        from . import mx, ops
+        value = getattr(mx if name in _MX else ops, name)
+        globals()[name] = value  # looked up once
+        return value
     raise AttributeError(name)

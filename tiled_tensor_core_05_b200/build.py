@@ -25,6 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libttc05.so")
 MX_LIB = os.path.join(PKG, "libttcmx.so")
+BIND = os.path.join(PKG, "_mxbind.so")  # CPython binding of libttcmx, against the torch in use
+BIND_SOURCE = "mx_bind.cpp"
 COMMON = ["host_common.cu"]  # linked into both libraries
 SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu"]
 MX_SOURCES = ["mx_api.cu", "mx_rows.cu", "mx_gemm_split.cu", "mx_gemm_pair.cu"]
@@ -45,16 +47,17 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in COMMON + SOURCES + MX_SOURCES + HEADERS]
+    files = [os.path.join(CSRC, s) for s in COMMON + SOURCES + MX_SOURCES + HEADERS + [BIND_SOURCE]]
     files += [os.path.join(INCLUDE, h) for h in ("gemm_f16.h", "gemm_mx.h")]
     files.append(os.path.abspath(__file__))
     return files
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MX_LIB):
+    built = (LIB, MX_LIB, BIND)
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MX_LIB))
+    t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -78,12 +81,39 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     sources = COMMON + SOURCES + MX_SOURCES
-    with cf.ThreadPoolExecutor(max_workers=len(sources)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
+        bind = ex.submit(_build_bind, verbose)
         objs = dict(zip(sources, ex.map(lambda s: _compile(s, ptxas_info, verbose), sources)))
+    bind.result()
     # only the extern "C" API is exported: gemm_* of libttc05, mx_* of libttcmx
     _link(MX_LIB, [objs[s] for s in COMMON + MX_SOURCES], "mx_*", verbose)
     _link(LIB, [objs[s] for s in COMMON + SOURCES], "gemm_*", verbose)
     return LIB
+
+
+def _build_bind(verbose: bool) -> None:
+    """The CPython extension: host code only, compiled against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib_dir = cpp_extension.library_paths()[0]
+    tmp = BIND + f".tmp{os.getpid()}"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", cuda]
+    for d in cpp_extension.include_paths():
+        cmd += ["-I", d]
+    cmd += [os.path.join(CSRC, BIND_SOURCE), "-o", tmp, "-L", lib_dir, f"-Wl,-rpath,{lib_dir}",
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
 
 
 def _link(lib: str, objs: list, exports: str, verbose: bool) -> None:

@@ -3,7 +3,9 @@ operands for the products of a linear layer.
 
 As in ``ops``, every function forwards device pointers, sizes, strides and the
 current CUDA stream of PyTorch to a C ABI (``include/gemm_mx.h``), whose CUDA
-kernels do all arithmetic; there is no fallback.
+kernels do all arithmetic; there is no fallback.  Checks of tensors and
+allocation of outputs are in a small CPython extension (``csrc/mx_bind.cpp``),
+since a call's kernels may take only a few microseconds.
 
     q = mx_quantize(w, "mxfp4")                  # weight (N, K), once
     y, h = rms_norm(x, g, residual=r, format="mxfp4")
@@ -16,6 +18,7 @@ elements of a row.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -28,7 +31,10 @@ FORMATS = {"mxfp8": 1, "mxfp4": 2}
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 BLOCK = 32
 
+BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mxbind.so")
+
 _lib = None
+_bind = None
 
 _p, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 _SIGNATURES = {
@@ -45,18 +51,24 @@ _SIGNATURES = {
 
 def mx_lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
-    global _lib
+    global _lib, _bind
     if _lib is None:
-        if not os.path.exists(LIB_PATH):
-            raise RuntimeError(
-                f"{LIB_PATH} is missing: build it with "
-                "`python -m tiled_tensor_core_05_b200.build` (there is no CPU fallback)")
+        for path in (LIB_PATH, BIND_PATH):
+            if not os.path.exists(path):
+                raise RuntimeError(
+                    f"{path} is missing: build it with "
+                    "`python -m tiled_tensor_core_05_b200.build` (there is no CPU fallback)")
         handle = ctypes.CDLL(LIB_PATH)
         for name, (args, res) in _SIGNATURES.items():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res
-        _lib = handle
+        spec = importlib.util.spec_from_file_location("_mxbind", BIND_PATH)
+        bind = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(bind)
+        bind.bind(*(ctypes.cast(getattr(handle, name), _p).value for name in
+                    ("mx_quantize", "mx_dequantize", "mx_rms_norm", "mx_gemm")))
+        _bind, _lib = bind, handle
     return _lib
 
 
@@ -151,40 +163,6 @@ def mx_untile_scales(scales: torch.Tensor, rows: int, cols: int) -> torch.Tensor
     return t[:rows, :-(-cols // BLOCK)]
 
 
-def _dtype(t: torch.Tensor, what: str) -> int:
-    """The code of the 16-bit type of the CUDA tensor ``t``."""
-    code = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    if code is None:
-        raise TypeError(f"{what} must be a torch.float16 or torch.bfloat16 tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    return code
-
-
-def _matrix(t: torch.Tensor, what: str, shape, dtype, device) -> int:
-    """Checks a matrix; its row stride in elements (of a single row, whose
-    stride means nothing, the columns rounded up to 8)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}")
-    if t.shape != shape or len(shape) != 2:
-        raise ValueError(f"{what} must be a matrix {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}")
-    step, unit = t.stride()
-    if unit != 1 and shape[1] > 1:
-        raise ValueError(f"the columns of {what} must be contiguous (stride(1) == 1)")
-    return step if shape[0] > 1 else (shape[1] + 7) // 8 * 8
-
-
-def _vector(t: torch.Tensor, what: str, n: int, dtype, device) -> int:
-    """Checks a vector; its address."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}")
-    if t.numel() != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{what} must be {n} contiguous values on {device}")
-    return t.data_ptr()
-
-
 def _mx(q: MxTensor, what: str) -> torch.device:
     """Checks an MX input; its device."""
     if not isinstance(q, MxTensor):
@@ -194,39 +172,36 @@ def _mx(q: MxTensor, what: str) -> torch.device:
     return q.data.device
 
 
-def _mx_out(q: MxTensor, rows: int, cols: int, format: str, device) -> None:
-    if _mx(q, "out") != device or q.rows != rows or q.cols != cols or q.format != format:
-        raise ValueError(f"out must be ({rows}, {cols}) {format} on {device}, got {q!r}")
+def _mx_out(q: MxTensor, x: torch.Tensor, format: str) -> None:
+    """Checks an MX output for the matrix x."""
+    if _mx(q, "out") != x.device or q.shape != tuple(x.shape) or q.format != format:
+        raise ValueError(f"out must be {tuple(x.shape)} {format} on {x.device}, got {q!r}")
 
 
-def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
-    """A new matrix whose rows start on 16 bytes."""
-    if cols % 8 == 0:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
-    return torch.empty((rows, _round(cols, 8)), dtype=dtype, device=device)[:, :cols]
+def _new_type(dtype: torch.dtype) -> int:
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be torch.float16 or torch.bfloat16")
+    return _DTYPES[dtype]
 
 
-def _alloc(stream, device, make, *args):
-    """make(*args) with the memory belonging to the stream that will write it."""
-    if stream is None:
-        return make(*args)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return make(*args)
+def _made(data: torch.Tensor, scales: torch.Tensor, ld: int, rows: int, cols: int,
+          format: str) -> MxTensor:
+    """An MxTensor of outputs the binding has allocated: right by construction."""
+    q = object.__new__(MxTensor)
+    q.data, q.scales, q.ld, q.rows, q.cols, q.format = data, scales, ld, rows, cols, format
+    return q
 
 
-def _call(name: str, device: torch.device, stream, *args) -> None:
-    """The library call, with ``device`` current, on ``stream`` or the device's
-    current stream."""
-    if torch._C._cuda_getDevice() != device.index:
-        with torch.cuda.device(device):
-            return _call(name, device, stream, *args)
-    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
-        ops._stream_handle(stream, device)
-    rc = getattr(_lib or mx_lib(), name)(*args, handle)
-    if rc:
-        ops._check(rc, name)
+def _handle(stream):
+    """None (the device's current stream) or the raw handle of a stream."""
+    return stream if stream is None else ops._stream_handle(stream, None)
+
+
+def _loaded():
+    """The binding, with the library loaded."""
+    if _bind is None:
+        mx_lib()
+    return _bind
 
 
 def mx_quantize(x: torch.Tensor, format: str, out: MxTensor | None = None, *,
@@ -236,15 +211,15 @@ def mx_quantize(x: torch.Tensor, format: str, out: MxTensor | None = None, *,
     quotient by its block's scale.  Asynchronous on ``stream`` (default: the
     current stream)."""
     fmt = _format(format)
-    dtype, dev, shape = _dtype(x, "x"), x.device, x.shape
-    ldx = _matrix(x, "x", shape, x.dtype, dev)
-    rows, cols = shape
+    bind = _bind or _loaded()
     if out is None:
-        out = _alloc(stream, dev, mx_empty, rows, cols, format, dev)
+        rc, data, scales, ld = bind.quantize(x, fmt, None, None, None, _handle(stream))
+        out = _made(data, scales, ld, *x.shape, format)
     else:
-        _mx_out(out, rows, cols, format, dev)
-    _call("mx_quantize", dev, stream, x.data_ptr(), out.data.data_ptr(), out.scales.data_ptr(),
-          rows, cols, ldx, out.ld, dtype, fmt)
+        _mx_out(out, x, format)
+        rc = bind.quantize(x, fmt, out.data, out.scales, out.ld, _handle(stream))[0]
+    if rc:
+        ops._check(rc, "mx_quantize")
     return out
 
 
@@ -252,15 +227,12 @@ def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float16,
                   out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
     """The values ``q`` stands for, rounded to ``dtype`` (fp16 or bf16; of
     ``out`` when given)."""
-    dev = _mx(q, "q")
-    if out is None:
-        if dtype not in _DTYPES:
-            raise TypeError("dtype must be torch.float16 or torch.bfloat16")
-        out = _alloc(stream, dev, _new, q.rows, q.cols, dtype, dev)
-    code = _dtype(out, "out")
-    ldx = _matrix(out, "out", (q.rows, q.cols), out.dtype, dev)
-    _call("mx_dequantize", dev, stream, q.data.data_ptr(), q.scales.data_ptr(), out.data_ptr(),
-          q.rows, q.cols, q.ld, ldx, code, FORMATS[q.format])
+    _mx(q, "q")
+    rc, out = (_bind or _loaded()).dequantize(
+        q.data, q.scales, q.rows, q.cols, q.ld, FORMATS[q.format], out,
+        _new_type(dtype) if out is None else None, _handle(stream))
+    if rc:
+        ops._check(rc, "mx_dequantize")
     return out
 
 
@@ -274,36 +246,25 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     of ``x``; "mxfp8" / "mxfp4" an :class:`MxTensor` for :func:`gemm_mx`,
     quantised without rounding in between.  ``residual_out`` may be ``x`` or
     ``residual`` itself (updated in place)."""
-    code, dtype, dev, shape = _dtype(x, "x"), x.dtype, x.device, x.shape
-    ldx = _matrix(x, "x", shape, dtype, dev)
-    rows, cols = shape
-    fmt = 0 if format is None else _format(format)
-    w = _vector(weight, "weight", cols, dtype, dev)
-    h = r = None
-    ldr = ldh = 0
-    if residual is not None:
-        ldr = _matrix(residual, "residual", shape, dtype, dev)
-        r = residual.data_ptr()
-        if residual_out is None:
-            residual_out = _alloc(stream, dev, _new, rows, cols, dtype, dev)
-        ldh = _matrix(residual_out, "residual_out", shape, dtype, dev)
-        h = residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    if fmt:
-        if out is None:
-            out = _alloc(stream, dev, mx_empty, rows, cols, format, dev)
-        else:
-            _mx_out(out, rows, cols, format, dev)
-        y, s, ldy = out.data.data_ptr(), out.scales.data_ptr(), out.ld
+    bind = _bind or _loaded()
+    if format is None:
+        rc, y, _, _, h = bind.rms_norm(x, weight, eps, residual, residual_out, 0, out, None, None,
+                                       _handle(stream))
+    elif out is None:
+        rc, data, scales, ld, h = bind.rms_norm(x, weight, eps, residual, residual_out,
+                                                _format(format), None, None, None,
+                                                _handle(stream))
+        y = _made(data, scales, ld, *x.shape, format)
     else:
-        if out is None:
-            out = _alloc(stream, dev, _new, rows, cols, dtype, dev)
-        ldy = _matrix(out, "out", shape, dtype, dev)
-        y, s = out.data_ptr(), None
-    _call("mx_rms_norm", dev, stream, x.data_ptr(), r, w, h, y, s, rows, cols, ldx, ldr, ldh, ldy,
-          eps, code, fmt)
-    return out if residual is None else (out, residual_out)
+        _mx_out(out, x, format)
+        rc, _, _, _, h = bind.rms_norm(x, weight, eps, residual, residual_out, _format(format),
+                                       out.data, out.scales, out.ld, _handle(stream))
+        y = out
+    if rc:
+        ops._check(rc, "mx_rms_norm")
+    if residual is None:
+        return y
+    return y, h if residual_out is None else residual_out
 
 
 def gemm_mx(a: MxTensor, b: MxTensor, bias: torch.Tensor | None = None, act: str | int = "none",
@@ -316,19 +277,14 @@ def gemm_mx(a: MxTensor, b: MxTensor, bias: torch.Tensor | None = None, act: str
     dev = _mx(a, "a")
     if _mx(b, "b") != dev or b.cols != a.cols or b.format != a.format:
         raise ValueError(f"a and b must share device, format and inner size: {a!r}, {b!r}")
-    M, N, K = a.rows, b.rows, a.cols
     act = ops._ACTS[act] if isinstance(act, str) else int(act)
-    if out is None:
-        if dtype not in _DTYPES:
-            raise TypeError("dtype must be torch.float16 or torch.bfloat16")
-        out = _alloc(stream, dev, _new, M, N, dtype, dev)
-    code = _dtype(out, "out")
-    ldc = _matrix(out, "out", (M, N), out.dtype, dev)
-    bias = None if bias is None else _vector(bias, "bias", N, out.dtype, dev)
-    _call("mx_gemm", dev, stream, a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(),
-          b.scales.data_ptr(), bias, out.data_ptr(), M, N, K, a.ld, b.ld, ldc, FORMATS[a.format],
-          code, act)
-    return out
+    rc, c = (_bind or _loaded()).gemm(
+        a.data, a.scales, b.data, b.scales, a.rows, b.rows, a.cols, a.ld, b.ld,
+        FORMATS[a.format], bias, act, out, _new_type(dtype) if out is None else None,
+        _handle(stream))
+    if rc:
+        ops._check(rc, "mx_gemm")
+    return c if out is None else out
 
 
 def mx_device_status(stream=None, device=None) -> int:
