@@ -96,10 +96,17 @@ int run_gemm(const MxGemmProblem& p) {
   rc = check_mx(p.A, p.SA, p.M, p.K, p.lda, p.format, d.device);
   if (rc == GEMM_OK) rc = check_mx(p.B, p.SB, p.N, p.K, p.ldb, p.format, d.device);
   if (rc != GEMM_OK) return rc;
-  // 256 x 256 tiles of a CTA pair once there are enough of them
-  const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  return p.M > 128 && tiles >= d.sm_count / 4 ? launch_mx_pair_gemm(p, d)
-                                              : launch_mx_split_gemm(p, d);
+  // The pair kernel's 256 x 256 tiles read half the bytes per product that the
+  // split kernel's 64 x 128 ones do, but need enough tiles, with most of their
+  // rows, to keep the SMs busy.  Measured: 1500 x 2000 x 2000 MXFP4 (48 pair
+  // tiles) 9.1 us as pairs, 13.3 split; 256 x 9000 x 4096 (36) 14.4 and 13.6; 128 x
+  // 18944 x 4096 (74, half empty; one wave of the split kernel) 15.9 and 14.8;
+  // 100 x 28672 x 8192 (112; two waves) 37.4 and 40.4.
+  const int64_t pair_tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+  const int64_t split_tiles = ((p.M + 63) / 64) * ((p.N + 127) / 128);
+  const bool pairs = p.M > 64 && pair_tiles >= d.sm_count / 4 &&
+                     (p.M > 128 || split_tiles > 2 * d.sm_count);
+  return pairs ? launch_mx_pair_gemm(p, d) : launch_mx_split_gemm(p, d);
 }
 
 }  // namespace

@@ -2,13 +2,17 @@
 // tiles with K split over a cluster.
 //
 // A tile is 128 rows of B (columns of C, the MMA's M) by BN rows of A (the
-// MMA's N: 16 to 128), so a single token wastes none of the weight's
+// MMA's N: 16 to 64), so a single token wastes none of the weight's
 // bandwidth.  The K range of a tile is split over the CTAs of a cluster; each
-// accumulates its part in TMEM, puts it in its own shared memory, and the
-// CTAs then add all parts in rank order through distributed shared memory,
-// each for its share of the tile.  Nothing is kept in device memory between
-// or during calls (no workspace, no counters), and the order of the sums is
-// fixed by the shape.
+// accumulates its part in TMEM and puts it in its own shared memory, sends
+// every other CTA the rows that one owns (one bulk copy between the SMs'
+// shared memories each), and adds the parts of its own rows in rank order.
+// Nothing is kept in device memory between or during calls (no workspace, no
+// counters), and the order of the sums is fixed by the shape.  Reading the
+// other CTAs' parts with loads instead runs at some 8 bytes a clock and SM (2 us
+// for 64 x 128 parts of two CTAs); it is done only for a few rows, where the
+// wait for the copies would cost more (1 x 8192 x 4096 MXFP4: 7.1 us, 7.6 with
+// copies; 16 x 2048 x 8192: 7.8 us, 6.8 with copies).
 //
 //   warp 0   TMA producer: elements by tensor maps into 128-byte-swizzled
 //            shared memory, scale tiles by plain bulk copies
@@ -28,22 +32,21 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kTileN = 128;  // columns of C per tile
 
-// Ring depths: kDeep stages leave room for two CTAs an SM (one for BN = 128:
-// two with 3 stages), 3 stages for three.
-constexpr int kShallow = 3;
-constexpr int kDeep = 5;
-constexpr int deep_stages(int bn) { return bn == 128 ? 3 : bn == 64 ? 4 : kDeep; }
+constexpr int kPullRows = 4;  // up to so many rows the parts are read, not sent
 
-template <int FMT, int BN, int STAGES>
+template <int FMT, int BN>
 struct SplitCfg {
-  static constexpr int kStages = STAGES;
+  static constexpr int kStages = BN == 64 ? 4 : 5;  // two CTAs an SM
   static constexpr int kWBytes = kTileN * kRowBytes;
   static constexpr int kXBytes = BN * kRowBytes;
   static constexpr int kSfBytes = Kind<FMT>::kSfTiles * kTileBytes;
   static constexpr int kStageBytes = kWBytes + kXBytes + 2 * kSfBytes;
-  static constexpr int kPartBytes = BN * kTileN * 4;  // fp32 partial tile, over the ring
-  static constexpr int kRing = kStages * kStageBytes > kPartBytes ? kStages * kStageBytes : kPartBytes;
-  static constexpr int kSmemBytes = 1024 + kRing + (2 * kStages + 2) * 8 + 16;
+  // over the ring: this CTA's fp32 part of the tile, then the parts of its rows
+  // that the others send
+  static constexpr int kPartBytes = BN * kTileN * 4;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kSmemBytes = 1024 + kRing + (2 * kStages + 3) * 8 + 16;
+  static_assert(2 * kPartBytes <= kRing, "parts");
   // accumulator, then one set of scales per stage: a stage's columns are
   // written again only after the MMAs that read them have completed
   static constexpr int kSfBase = BN < 32 ? 32 : BN;
@@ -83,6 +86,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float4& y) {
+  v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+  v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+}
+
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
@@ -107,12 +115,12 @@ __device__ __forceinline__ void store_row8(const SplitArgs& a, int m, int n, con
   store8(a.C + static_cast<int64_t>(m) * a.ldc + n, pack8<T>(y), count);
 }
 
-template <int FMT, int BN, int STAGES>
+template <int FMT, int BN>
 __global__ void __launch_bounds__(kThreads)
     split_gemm_kernel(const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmA, const SplitArgs a) {
-  using Cfg = SplitCfg<FMT, BN, STAGES>;
-  constexpr int kStages = STAGES;
+  using Cfg = SplitCfg<FMT, BN>;
+  constexpr int kStages = Cfg::kStages;
   constexpr int kSfTiles = Kind<FMT>::kSfTiles;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -123,7 +131,8 @@ __global__ void __launch_bounds__(kThreads)
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* drain = acc_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* received = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(received + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -137,6 +146,11 @@ __global__ void __launch_bounds__(kThreads)
   const int s_begin = static_cast<int>(static_cast<int64_t>(a.stages) * rank / splits);
   const int s_end = static_cast<int>(static_cast<int64_t>(a.stages) * (rank + 1) / splits);
 
+  // the rows of the tile that rank r finishes are [first_row(r), first_row(r + 1))
+  auto first_row = [&](int r) { return rows * r / splits; };
+  const int r0 = first_row(rank), r1 = first_row(rank + 1);
+  const int slot_bytes = (BN + splits - 1) / splits * kTileN * 4;
+
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -144,6 +158,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
+    mbar_init(received, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmB);
@@ -276,33 +291,68 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncwarp();
   tc_fence_before_sync();
-  if (splits > 1)
-    cluster_sync();
-  else
+  uint8_t* incoming = smem + Cfg::kPartBytes;
+  const bool pull = rows <= kPullRows;
+  if (splits > 1) {
+    fence_proxy_async_smem();  // the part is read by bulk copies
+    cluster_sync();            // all parts are written, all rings free
+    if (!pull && threadIdx.x == 0 && *abort_flag == 0) {
+      mbar_arrive_expect_tx(received,
+                            static_cast<uint32_t>((splits - 1) * (r1 - r0) * kTileN * 4));
+      for (int k = 1; k < splits; ++k) {
+        const int to = rank + k < splits ? rank + k : rank + k - splits;
+        const int from_row = first_row(to), n = first_row(to + 1) - from_row;
+        if (n == 0) continue;
+        // the receiver keeps its slots in rank order, without its own
+        const int slot = rank < to ? rank : rank - 1;
+        bulk_push(map_to_cta(smem_u32(incoming) + static_cast<uint32_t>(slot * slot_bytes),
+                             static_cast<uint32_t>(to)),
+                  smem + from_row * kTileN * 4, static_cast<uint32_t>(n * kTileN * 4),
+                  map_to_cta(smem_u32(received), static_cast<uint32_t>(to)));
+      }
+    }
+    if (!pull && r1 > r0 && *abort_flag == 0 && !mbar_wait(received, 0, abort_flag, a.timeout_ns))
+      raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 2);
+  } else {
     __syncthreads();
+  }
 
-  // items: (row, 8 columns), dealt out over the threads of the whole cluster
-  const uint32_t part = smem_u32(smem);
-  if (*abort_flag == 0) {
+  auto store = [&](int m, int n, const float (&v)[8]) {
+    if (a.dtype == MX_F16)
+      store_row8<__half>(a, m, n, v);
+    else
+      store_row8<__nv_bfloat16>(a, m, n, v);
+  };
+  if (*abort_flag == 0 && splits > 1 && pull) {
+    // items: 8 columns of a row, dealt out over the threads of the cluster
     for (int it = rank * kThreads + threadIdx.x; it < rows * (kTileN / 8); it += splits * kThreads) {
-      const int m = it >> 4, n = n0 + (it & 15) * 8;
-      if (n >= a.N) continue;
-      const uint32_t at = part + static_cast<uint32_t>(m * kTileN + (it & 15) * 8) * 4;
+      const int m = it >> 4, c = (it & 15) * 8;
+      if (n0 + c >= a.N) continue;
       float v[8] = {};
       for (int s = 0; s < splits; ++s) {
-        const uint32_t src = map_to_cta(at, static_cast<uint32_t>(s));
-        const float4 x = ld_cluster_f4(src), y = ld_cluster_f4(src + 16);
-        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-        v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        const uint32_t src = map_to_cta(
+            smem_u32(smem) + static_cast<uint32_t>(m * kTileN + c) * 4, static_cast<uint32_t>(s));
+        add8(v, ld_cluster_f4(src), ld_cluster_f4(src + 16));
       }
-      if (a.dtype == MX_F16)
-        store_row8<__half>(a, m0 + m, n, v);
-      else
-        store_row8<__nv_bfloat16>(a, m0 + m, n, v);
+      store(m0 + m, n0 + c, v);
+    }
+  } else if (*abort_flag == 0) {
+    // items: 8 columns of one of this CTA's rows
+    for (int it = threadIdx.x; it < (r1 - r0) * (kTileN / 8); it += kThreads) {
+      const int m = it >> 4, c = (it & 15) * 8;
+      if (n0 + c >= a.N) continue;
+      float v[8] = {};
+      for (int s = 0; s < splits; ++s) {
+        const uint8_t* base = s == rank ? smem + r0 * kTileN * 4
+                                        : incoming + (s < rank ? s : s - 1) * slot_bytes;
+        const float4* src = reinterpret_cast<const float4*>(base) + (m * kTileN + c) / 4;
+        add8(v, src[0], src[1]);
+      }
+      store(m0 + r0 + m, n0 + c, v);
     }
   }
   __syncwarp();
-  // no CTA leaves while another may still read its part
+  // no CTA leaves while another, or its own copies, may still read its shared memory
   if (splits > 1)
     cluster_sync();
   else
@@ -319,26 +369,22 @@ struct Residency {
   std::atomic<int> clusters[9] = {};
 };
 
-// Into how many parts of at least two k-blocks K is divided: as many as run in
-// one wave, since a second wave costs more than the division brings
-// (14336 x 4096 MXFP8 for one token: 12.5 us as 3 x 112 CTAs, 17.7 as 4 x 112).
-// Larger clusters take a place an SM only, where they find it sooner and the
-// joining of many parts costs as much as it saves (16 x 4096 x 8192 MXFP4, 32
-// tiles: 4 parts 8.5 us, 5 parts 9.0, 8 parts 9.1; 60 x 8192 x 4096, 64 tiles
-// of 64 rows: 2 parts 10.0 us, 3 parts 11.6).
-template <int FMT, int BN, int STAGES>
+// Into how many parts of at least four k-blocks K is divided: as many as run in
+// one wave, since a second wave costs more than the division brings (32 x 8192
+// x 4096 MXFP8, 64 tiles: 1 part 15.8 us, 2 parts 11.5, 4 parts 10.2, 5 parts 16.2).
+template <int FMT, int BN>
 int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
-  using Cfg = SplitCfg<FMT, BN, STAGES>;
+  using Cfg = SplitCfg<FMT, BN>;
   static Residency residency[64];
   int splits = 1;
-  for (int c = 2; c <= 8 && stages >= 2 * c; ++c) {
+  for (int c = 2; c <= 8 && stages >= 4 * c; ++c) {
     std::atomic<int>& known = residency[d.device & 63].clusters[c];
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
       Launch l(dim3(static_cast<unsigned>(c * d.sm_count)), dim3(kThreads), Cfg::kSmemBytes,
                nullptr);
       l.cluster(static_cast<unsigned>(c));
-      if (cudaOccupancyMaxActiveClusters(&n, split_gemm_kernel<FMT, BN, STAGES>, &l.cfg) !=
+      if (cudaOccupancyMaxActiveClusters(&n, split_gemm_kernel<FMT, BN>, &l.cfg) !=
               cudaSuccess ||
           n <= 0) {
         cudaGetLastError();
@@ -346,17 +392,16 @@ int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
       }
       known.store(n, std::memory_order_relaxed);
     }
-    const bool dense = c == 2 || (c == 3 && BN <= 32);
-    if (tiles <= static_cast<int64_t>(n) * (dense ? Cfg::kPerSm : 1)) splits = c;
+    if (tiles <= static_cast<int64_t>(n) * Cfg::kPerSm) splits = c;
   }
   return splits;
 }
 
-template <int FMT, int BN, int STAGES>
+template <int FMT, int BN>
 bool set_attributes(const DeviceCtx& d) {
   static std::atomic<uint64_t> attr_done{0};
-  auto kern = split_gemm_kernel<FMT, BN, STAGES>;
-  using Cfg = SplitCfg<FMT, BN, STAGES>;
+  auto kern = split_gemm_kernel<FMT, BN>;
+  using Cfg = SplitCfg<FMT, BN>;
   const uint64_t bit = 1ull << (d.device & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -372,10 +417,10 @@ bool set_attributes(const DeviceCtx& d) {
   return true;
 }
 
-template <int FMT, int BN, int STAGES>
+template <int FMT, int BN>
 int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
-  using Cfg = SplitCfg<FMT, BN, STAGES>;
-  auto kern = split_gemm_kernel<FMT, BN, STAGES>;
+  using Cfg = SplitCfg<FMT, BN>;
+  auto kern = split_gemm_kernel<FMT, BN>;
   const int64_t row_bytes = mx_row_bytes(p.K, FMT);
   CUtensorMap tB, tA;
   int rc = encode_tmap_u8_2d(&tB, p.B, row_bytes, p.N, p.ldb, kTileN);
@@ -407,32 +452,19 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
-// Up to 16 rows: three CTAs an SM where that divides K further than two of a
-// deeper ring (12.5 us instead of 13.4 above); else the deeper ring (32 x
-// 28672 x 8192 MXFP4: 22.6 us instead of 24.4).
 template <int FMT, int BN>
-int launch_depth(const MxGemmProblem& p, const DeviceCtx& d) {
-  constexpr int kStages = deep_stages(BN);
-  if (!set_attributes<FMT, BN, kStages>(d)) return GEMM_ERR_LAUNCH;
+int launch_tile(const MxGemmProblem& p, const DeviceCtx& d) {
+  if (!set_attributes<FMT, BN>(d)) return GEMM_ERR_LAUNCH;
   const int64_t tiles = (p.M + BN - 1) / BN * ((p.N + kTileN - 1) / kTileN);
   const int64_t stages = (mx_row_bytes(p.K, FMT) + kRowBytes - 1) / kRowBytes;
-  const int deep = choose_splits<FMT, BN, kStages>(tiles, stages, d);
-  if constexpr (BN == 16) {
-    if (!set_attributes<FMT, BN, kShallow>(d)) return GEMM_ERR_LAUNCH;
-    const int shallow = choose_splits<FMT, BN, kShallow>(tiles, stages, d);
-    if (shallow > deep) return launch<FMT, BN, kShallow>(p, d, shallow);
-  }
-  return launch<FMT, BN, kStages>(p, d, deep);
+  return launch<FMT, BN>(p, d, choose_splits<FMT, BN>(tiles, stages, d));
 }
 
 template <int FMT>
 int launch_rows(const MxGemmProblem& p, const DeviceCtx& d) {
-  if (p.M <= 16) return launch_depth<FMT, 16>(p, d);
-  if (p.M <= 32) return launch_depth<FMT, 32>(p, d);
-  // 64 rows a tile as long as 128 would leave most SMs without one
-  const int64_t tiles128 = (p.M + 127) / 128 * ((p.N + 127) / 128);
-  if (p.M <= 64 || tiles128 < d.sm_count / 2) return launch_depth<FMT, 64>(p, d);
-  return launch_depth<FMT, 128>(p, d);
+  if (p.M <= 16) return launch_tile<FMT, 16>(p, d);
+  if (p.M <= 32) return launch_tile<FMT, 32>(p, d);
+  return launch_tile<FMT, 64>(p, d);
 }
 
 template <class T>

@@ -85,6 +85,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Copy of `bytes` (a multiple of 16) from this CTA's shared memory to that of
+// another CTA of the cluster, counted on an mbarrier there (shared::cluster
+// addresses).
+__device__ __forceinline__ void bulk_push(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];" ::"r"(dst),
+      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // bias + activation in fp32 of two columns.
 __device__ __forceinline__ float2 finish2(float2 v, float2 b, int act) {
   v = __fadd2_rn(v, b);
