@@ -432,6 +432,97 @@ def test_streams_and_graph_replay():
         assert torch.equal(c, v)
 
 
+def test_threads_on_their_own_streams():
+    """Four host threads, each on a stream of its own, calling every operator at once."""
+    import threading
+    t = torch.float16
+    rng = np.random.default_rng(21)
+    g = dev_vec(host16(1 + 0.1 * rng.standard_normal(384), t), t)
+    weights = [ttc.mx_quantize(dev16(host16(0.05 * rng.standard_normal((n, 384)), t), t), "mxfp8")
+               for n in (200, 3000)]
+    xs = [dev16(host16(rng.standard_normal((m, 384)), t), t) for m in (1, 30, 100, 1000)]
+
+    def chain(x):
+        q = ttc.rms_norm(x, g, format="mxfp8")
+        return [ttc.mx_dequantize(q)] + [ttc.gemm_mx(q, w, act="gelu") for w in weights]
+
+    want = [chain(x) for x in xs]
+    torch.cuda.synchronize()
+    errors = []
+
+    def worker(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                got = [(i, chain(xs[i])) for _ in range(5) for i in ((k + j) % 4 for j in range(4))]
+                stream.synchronize()
+            for i, c in got:
+                if not all(torch.equal(u, v) for u, v in zip(c, want[i])):
+                    errors.append((k, i))
+        except Exception as e:
+            errors.append((k, repr(e)))
+
+    threads = [threading.Thread(target=worker, args=(k,)) for k in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join(timeout=120)
+    assert not any(th.is_alive() for th in threads) and not errors, errors
+
+
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+def test_offsets_past_32_bits(fmt):
+    """Inputs and outputs of more than 2^32 bytes: the first and last rows and some between."""
+    t = torch.bfloat16
+    rows, cols = 66000, 33000
+    x = torch.zeros((rows, cols), dtype=t, device="cuda")
+    pick = [0, 1, 65, 32768, 65075, 65076, rows - 130, rows - 1]  # 65076 x 33000 passes 2^31
+    rng = np.random.default_rng(0)
+    v = host16(rng.standard_normal((len(pick), cols)), t)
+    x[pick] = torch.from_numpy(v).to(t).cuda()
+    q = ttc.mx_quantize(x, fmt)
+    codes, scales = ref.quantize(v, fmt)
+    assert np.array_equal(q.data[pick].cpu().numpy()[:, :ref.row_bytes(cols, fmt)],
+                          ref.pack(codes, fmt))
+    blocks = ttc.mx_untile_scales(q.scales, rows, cols)[pick].cpu().numpy()
+    assert np.array_equal(blocks, scales)
+    x.fill_(1.0)
+    ttc.mx_dequantize(q, out=x)
+    assert np.array_equal(ref.to_np(x[pick]), ref.values(codes, scales, fmt))
+    w = dev_vec(np.ones(cols), t)
+    y = ttc.rms_norm(x, w, 1e-6, out=x)
+    assert np.array_equal(ref.to_np(y[pick]),
+                          ref.round_to(ref.norm(ref.values(codes, scales, fmt), np.ones(cols), 1e-6), t))
+    del x, y, q
+    # C of 66000 x 33000
+    K = 64
+    a = np.zeros((rows, K), np.uint8)
+    sa = np.full((rows, 2), 127, np.uint8)
+    small, one = exact_operand(rng, len(pick), K, fmt), exact_operand(rng, cols, K, fmt)
+    a[pick], sa[pick] = small
+    c = ttc.gemm_mx(make_mx(a, sa, fmt), make_mx(*one, fmt), dtype=t)
+    want = ref.values(*small, fmt) @ ref.values(*one, fmt).T
+    assert np.array_equal(ref.to_np(c[pick]), ref.round_to(want, t))
+    assert int((c != 0).any(1).sum()) <= len(pick)
+
+
+@pytest.mark.parametrize("cols", [300, 20000])
+def test_rms_norm_without_keeping_the_sum(cols):
+    """The C entry point with a residual and no place for h."""
+    t = torch.float16
+    rng = np.random.default_rng(cols)
+    x, r = (host16(rng.standard_normal((5, cols)), t) for _ in range(2))
+    w = host16(1 + 0.1 * rng.standard_normal(cols), t)
+    dx, dr, dw, y = dev16(x, t), dev16(r, t), dev_vec(w, t), dev16(np.zeros((5, cols)), t)
+    ld = dx.stride(0)
+    assert raw("mx_rms_norm", dx.data_ptr(), dr.data_ptr(), dw.data_ptr(), None, y.data_ptr(), None,
+               5, cols, ld, ld, 0, ld, 1e-6, 0, 0) == 0
+    h = ref.round_to(x + r, t)
+    eps = float(np.float32(1e-6))
+    assert np.array_equal(ref.to_np(y), ref.round_to(ref.norm(h, w, eps), t))
+    assert np.array_equal(ref.to_np(dx), x) and np.array_equal(ref.to_np(dr), r)
+
+
 def test_same_bits_on_every_run():
     rng = np.random.default_rng(11)
     a = make_mx(*random_operand(rng, 40, 5000, "mxfp8", 1.0), "mxfp8")
