@@ -266,20 +266,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sfb = sfa + Kind<FMT>::kSfCols;
 #pragma unroll
           for (int t = 0; t < Kind<FMT>::kSfTiles; ++t) {
-            copy_scales<2>(sfa + 4 * t, scale_desc(s_addr + t * kTileBytes));
-            copy_scales<2>(sfb + 8 * t, scale_desc(s_addr + Cfg::kSf + t * kTileBytes));
-            copy_scales<2>(sfb + 8 * t + 4, scale_desc(s_addr + 2 * Cfg::kSf + t * kTileBytes));
+            copy_scales<2>(sfa + 4 * t, (s_addr + t * kTileBytes) >> 4);
+            copy_scales<2>(sfb + 8 * t, (s_addr + Cfg::kSf + t * kTileBytes) >> 4);
+            copy_scales<2>(sfb + 8 * t + 4, (s_addr + 2 * Cfg::kSf + t * kTileBytes) >> 4);
           }
-          const int left = a.row_bytes - kb * kRowBytes;
-#pragma unroll
-          for (int k = 0; k < kMmasPerStage; ++k) {
-            if (k * kMmaBytes >= left) break;
-            const int t = FMT == MX_FP8 ? 0 : k / 2;
-            mx_mma<FMT, 2>(d, smem_desc_sw128(a_addr + k * kMmaBytes, 16, 1024),
-                           smem_desc_sw128(b_addr + k * kMmaBytes, 16, 1024),
-                           mx_idesc<FMT>(kTile, kTile, k), sfa + 4 * t, sfb + 8 * t,
-                           (i | k) != 0 ? 1u : 0u);
-          }
+          issue_mmas<FMT, 2, kTile, kTile, 8>(d, a_addr, b_addr, sfa, sfb,
+                                              a.row_bytes - kb * kRowBytes, i != 0);
           umma_commit_pair(&empty[stage], 0x3);  // stage free in both CTAs
           if (++stage == kStages) {
             stage = 0;

@@ -238,20 +238,11 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int t = 0; t < kSfTiles; ++t) {
           if (t >= have) break;
-          copy_scales<1>(sfw + 4 * t, scale_desc(s_addr + t * kTileBytes));
-          copy_scales<1>(sfx + 4 * t, scale_desc(s_addr + Cfg::kSfBytes + t * kTileBytes));
+          copy_scales<1>(sfw + 4 * t, (s_addr + t * kTileBytes) >> 4);
+          copy_scales<1>(sfx + 4 * t, (s_addr + Cfg::kSfBytes + t * kTileBytes) >> 4);
         }
-        // the last stage: only the MMAs that reach into the row
-        const int left = a.row_bytes - s * kRowBytes;
-#pragma unroll
-        for (int k = 0; k < kMmasPerStage; ++k) {
-          if (k * kMmaBytes >= left) break;
-          const int t = FMT == MX_FP8 ? 0 : k / 2;
-          mx_mma<FMT, 1>(tmem, smem_desc_sw128(w_addr + k * kMmaBytes, 16, 1024),
-                         smem_desc_sw128(x_addr + k * kMmaBytes, 16, 1024),
-                         mx_idesc<FMT>(kTileN, BN, k), sfw + 4 * t, sfx + 4 * t + half,
-                         (s != s_begin || k != 0) ? 1u : 0u);
-        }
+        issue_mmas<FMT, 1, kTileN, BN, 4>(tmem, w_addr, x_addr, sfw, sfx + half,
+                                          a.row_bytes - s * kRowBytes, s != s_begin);
         umma_commit(&empty[stage]);
         if (++stage == kStages) {
           stage = 0;

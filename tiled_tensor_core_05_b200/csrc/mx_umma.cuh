@@ -8,6 +8,8 @@
 // elements = two.
 #pragma once
 
+#include <type_traits>
+
 #include "mx_common.cuh"
 
 namespace ttc {
@@ -36,33 +38,46 @@ __host__ __device__ constexpr uint32_t mx_idesc(int m, int n, int k) {
          (static_cast<uint32_t>(m >> 7) << 27) | (id << 29);
 }
 
-// Descriptor of a scale tile: 32 rows of 16 bytes, no swizzle, 8-row groups
-// 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(128u >> 4) << 32 |
-         static_cast<uint64_t>(1u) << 46;
-}
+// Descriptors: an operand's rows of 128 bytes, 128-byte swizzled, K-major
+// (smem_desc_sw128); a scale tile's 32 rows of 16 bytes, no swizzle, 8-row
+// groups 128 bytes apart.
+//
+// One thread issues all of this, and its instructions are what a k-block's
+// time comes down to, so descriptors are two 32-bit words of which only the
+// low one changes (address >> 4; nothing carries out of it), and what can be
+// is a constant.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kScaleDescHigh = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 
-// A scale tile from shared memory to 4 TMEM columns, repeated in the four
-// 32-lane quarters: lane l, column c holds the scales of row 32 c + l.
+// A scale tile from shared memory (address >> 4) to 4 TMEM columns, repeated in
+// the four 32-lane quarters: lane l, column c holds the scales of row 32 c + l.
 template <int CTAS>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t low) {
   if constexpr (CTAS == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(low), "r"(kScaleDescHigh)
+        : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(low), "r"(kScaleDescHigh)
+        : "memory");
 }
 
-// D (+)= (A . SA) (B . SB), fp32 accumulator.
+// D (+)= (A . SA) (B . SB), fp32 accumulator; a, b: low descriptor words.
 #define TTC_MX_MMA(GROUP, KIND)                                                                   \
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                  \
-               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;" \
-               "\n\t}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)  \
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %7};\n\t"             \
+               "mov.b64 db, {%2, %7};\n\tsetp.ne.b32 p, %6, 0;\n\t"                               \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], da, db, %3, [%4], [%5], p;" \
+               "\n\t}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate),  \
+               "r"(kDescHigh)                                                                     \
                : "memory")
 template <int FMT, int CTAS>
-__device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mx_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
   if constexpr (FMT == MX_FP8 && CTAS == 1)
     TTC_MX_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
@@ -74,6 +89,31 @@ __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint3
     TTC_MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
 }
 #undef TTC_MX_MMA
+
+// The MMAs of one k-block into d: A of MMA shape M x N from a, B from b (shared
+// addresses), scales of A from column sa and of B from sb on, 4 and
+// SB_TILE columns per scale tile; `left` bytes of the row remain.
+template <int FMT, int CTAS, int M, int N, int SB_TILE>
+__device__ __forceinline__ void issue_mmas(uint32_t d, uint32_t a, uint32_t b, uint32_t sa,
+                                           uint32_t sb, int left, bool accumulate) {
+  const uint32_t al = desc_low(a), bl = desc_low(b);
+  auto one = [&](auto k, uint32_t acc) {
+    constexpr int K = decltype(k)::value;
+    constexpr int t = FMT == MX_FP8 ? 0 : K / 2;
+    mx_mma<FMT, CTAS>(d, al + K * (kMmaBytes >> 4), bl + K * (kMmaBytes >> 4),
+                      mx_idesc<FMT>(M, N, K), sa + 4 * t, sb + SB_TILE * t, acc);
+  };
+  one(std::integral_constant<int, 0>{}, accumulate ? 1u : 0u);
+  if (left >= kRowBytes) {
+    one(std::integral_constant<int, 1>{}, 1u);
+    one(std::integral_constant<int, 2>{}, 1u);
+    one(std::integral_constant<int, 3>{}, 1u);
+  } else {  // the last k-block: only the MMAs that reach into the row
+    if (left > 1 * kMmaBytes) one(std::integral_constant<int, 1>{}, 1u);
+    if (left > 2 * kMmaBytes) one(std::integral_constant<int, 2>{}, 1u);
+    if (left > 3 * kMmaBytes) one(std::integral_constant<int, 3>{}, 1u);
+  }
+}
 
 // Untiled copy of `bytes` (a multiple of 16) global -> shared, counted on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
