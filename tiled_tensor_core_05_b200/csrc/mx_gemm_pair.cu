@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer (leader) ---
-    if (leader && lane == 0) {
+    if (leader) {
+      const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
       int stage = 0;
       uint32_t phase = 0, down = 0;
       int buf = 0;
@@ -235,58 +236,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int site = 0;
       for (int tile = pair; tile < num_tiles && ok; tile += npairs, down ^= 1u) {
-        if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, a.timeout_ns)) {
-          ok = false;
+        ok = mbar_wait_warp(&acc_empty[buf], acc_phase ^ 1u, abort_flag, a.timeout_ns);
+        if (!ok) {
           site = 5;
           break;
         }
         if (tile != pair) {  // the previous tile's epilogue has read the shared columns
-          if (!mbar_wait(shared_empty, shared_phase, abort_flag, a.timeout_ns)) {
-            ok = false;
+          ok = mbar_wait_warp(shared_empty, shared_phase, abort_flag, a.timeout_ns);
+          if (!ok) {
             site = 7;
             break;
           }
           shared_phase ^= 1u;
         }
         tc_fence_after_sync();
-        const uint32_t d = tmem + static_cast<uint32_t>(buf ? Cfg::kAcc1 : 0);
+        const uint32_t d = base + static_cast<uint32_t>(buf ? Cfg::kAcc1 : 0);
         for (int i = 0; i < a.num_kb; ++i) {
           const int kb = down ? a.num_kb - 1 - i : i;
-          if (!mbar_wait(&full[stage], phase, abort_flag, a.timeout_ns)) {
-            ok = false;
+          ok = mbar_wait_warp(&full[stage], phase, abort_flag, a.timeout_ns);
+          if (!ok) {
             site = 6;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a_addr = smem_u32(smA + stage * Cfg::kOperand);
-          const uint32_t b_addr = smem_u32(smB + stage * Cfg::kOperand);
-          const uint32_t s_addr = smem_u32(smS + stage * 3 * Cfg::kSf);
-          // columns: 4 per tile of A's scales, then 8 per tile of B's (256 rows)
-          const uint32_t sfa = tmem + Cfg::kSfBase + static_cast<uint32_t>(stage * Cfg::kSetCols);
-          const uint32_t sfb = sfa + Kind<FMT>::kSfCols;
+          if (elect_one()) {
+            const uint32_t s_addr = smem_u32(smS + stage * 3 * Cfg::kSf);
+            // columns: 4 per tile of A's scales, then 8 per tile of B's (256 rows)
+            const uint32_t sfa = base + Cfg::kSfBase + static_cast<uint32_t>(stage * Cfg::kSetCols);
+            const uint32_t sfb = sfa + Kind<FMT>::kSfCols;
 #pragma unroll
-          for (int t = 0; t < Kind<FMT>::kSfTiles; ++t) {
-            copy_scales<2>(sfa + 4 * t, (s_addr + t * kTileBytes) >> 4);
-            copy_scales<2>(sfb + 8 * t, (s_addr + Cfg::kSf + t * kTileBytes) >> 4);
-            copy_scales<2>(sfb + 8 * t + 4, (s_addr + 2 * Cfg::kSf + t * kTileBytes) >> 4);
+            for (int t = 0; t < Kind<FMT>::kSfTiles; ++t) {
+              copy_scales<2>(sfa + 4 * t, (s_addr + t * kTileBytes) >> 4);
+              copy_scales<2>(sfb + 8 * t, (s_addr + Cfg::kSf + t * kTileBytes) >> 4);
+              copy_scales<2>(sfb + 8 * t + 4, (s_addr + 2 * Cfg::kSf + t * kTileBytes) >> 4);
+            }
+            issue_mmas<FMT, 2, kTile, kTile, 8>(d, smem_u32(smA + stage * Cfg::kOperand),
+                                                smem_u32(smB + stage * Cfg::kOperand), sfa, sfb,
+                                                a.row_bytes - kb * kRowBytes, i != 0);
+            umma_commit_pair(&empty[stage], 0x3);  // stage free in both CTAs
+            if (i == a.num_kb - 1) umma_commit_pair(&acc_full[buf], 0x3);  // both epilogues may read
           }
-          issue_mmas<FMT, 2, kTile, kTile, 8>(d, a_addr, b_addr, sfa, sfb,
-                                              a.row_bytes - kb * kRowBytes, i != 0);
-          umma_commit_pair(&empty[stage], 0x3);  // stage free in both CTAs
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair(&acc_full[buf], 0x3);  // both epilogues may read
         buf ^= 1;
         if (buf == 0) acc_phase ^= 1u;
       }
       if (!ok) {
-        raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleMma << 4) | site);
-        umma_commit_pair(drain, 0x1);
-        (void)mbar_wait(drain, 0, nullptr, a.timeout_ns);
+        if (elect_one()) {
+          raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleMma << 4) | site);
+          umma_commit_pair(drain, 0x1);
+          (void)mbar_wait(drain, 0, nullptr, a.timeout_ns);
+        }
+        __syncwarp();
       }
     }
   } else {

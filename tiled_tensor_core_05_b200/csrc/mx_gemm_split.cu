@@ -217,23 +217,20 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int s = s_begin; s < s_end; ++s) {
-        if (!mbar_wait(&full[stage], phase, abort_flag, a.timeout_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t w_addr = smem_u32(smW + stage * Cfg::kWBytes);
-        const uint32_t x_addr = smem_u32(smX + stage * Cfg::kXBytes);
+    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+    // rows 64 .. 127 of a scale tile are its columns 2 and 3
+    const uint32_t half = BN == 64 ? static_cast<uint32_t>(mt & 1) * 2u : 0u;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int s = s_begin; s < s_end; ++s) {
+      ok = mbar_wait_warp(&full[stage], phase, abort_flag, a.timeout_ns);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
         const uint32_t s_addr = smem_u32(smS + stage * 2 * Cfg::kSfBytes);
-        const uint32_t sfw = tmem + Cfg::kSfBase + stage * 2 * Kind<FMT>::kSfCols;
+        const uint32_t sfw = base + Cfg::kSfBase + stage * 2 * Kind<FMT>::kSfCols;
         const uint32_t sfx = sfw + Kind<FMT>::kSfCols;
-        // rows 64 .. 127 of a scale tile are its columns 2 and 3
-        const uint32_t half = BN == 64 ? static_cast<uint32_t>(mt & 1) * 2u : 0u;
         const int have = min(kSfTiles, a.tiles - s * kSfTiles);
 #pragma unroll
         for (int t = 0; t < kSfTiles; ++t) {
@@ -241,21 +238,25 @@ __global__ void __launch_bounds__(kThreads)
           copy_scales<1>(sfw + 4 * t, (s_addr + t * kTileBytes) >> 4);
           copy_scales<1>(sfx + 4 * t, (s_addr + Cfg::kSfBytes + t * kTileBytes) >> 4);
         }
-        issue_mmas<FMT, 1, kTileN, BN, 4>(tmem, w_addr, x_addr, sfw, sfx + half,
+        issue_mmas<FMT, 1, kTileN, BN, 4>(base, smem_u32(smW + stage * Cfg::kWBytes),
+                                          smem_u32(smX + stage * Cfg::kXBytes), sfw, sfx + half,
                                           a.row_bytes - s * kRowBytes, s != s_begin);
         umma_commit(&empty[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (s == s_end - 1) umma_commit(acc_full);
       }
-      if (ok) {
-        umma_commit(acc_full);
-      } else {
+      __syncwarp();
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {
+      if (elect_one()) {
         raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleMma << 4) | 1);
         umma_commit(drain);
         (void)mbar_wait(drain, 0, nullptr, a.timeout_ns);
       }
+      __syncwarp();
     }
   } else {
     int ok = 1;

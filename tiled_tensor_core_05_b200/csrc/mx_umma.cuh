@@ -38,6 +38,23 @@ __host__ __device__ constexpr uint32_t mx_idesc(int m, int n, int k) {
          (static_cast<uint32_t>(m >> 7) << 27) | (id << 29);
 }
 
+// The MMA warp runs its loop as a whole, so that descriptors and addresses stay
+// in uniform registers (a lane of its own would move every operand of every
+// instruction there: 404 instead of %%% us at 8192^3 MXFP8); one elected lane
+// issues.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                               const volatile int* abort_flag,
+                                               uint64_t timeout_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, timeout_ns)) != 0;
+}
+
 // Descriptors: an operand's rows of 128 bytes, 128-byte swizzled, K-major
 // (smem_desc_sw128); a scale tile's 32 rows of 16 bytes, no swizzle, 8-row
 // groups 128 bytes apart.
