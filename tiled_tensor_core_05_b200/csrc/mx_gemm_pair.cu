@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Cfg::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
@@ -178,21 +178,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // --------------------------------------------- TMA producer (both CTAs) ---
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, parity = 0, down = 0;
-      bool ok = true;
-      for (int tile = pair; tile < num_tiles && ok; tile += npairs, down ^= 1u) {
-        int mb, nb;
-        tile_coords(tile, num_m, num_n, a.group_m, mb, nb);
-        const int a_row = mb * kTile + rank * kHalf;
-        const int b_row = nb * kTile + rank * kHalf;
-        for (int i = 0; i < a.num_kb; ++i) {
-          const int kb = down ? a.num_kb - 1 - i : i;
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns)) {
-            ok = false;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, parity = 0, down = 0;
+    bool ok = true;
+    for (int tile = pair; tile < num_tiles && ok; tile += npairs, down ^= 1u) {
+      int mb, nb;
+      tile_coords(tile, num_m, num_n, a.group_m, mb, nb);
+      const int a_row = mb * kTile + rank * kHalf;
+      const int b_row = nb * kTile + rank * kHalf;
+      for (int i = 0; i < a.num_kb; ++i) {
+        const int kb = down ? a.num_kb - 1 - i : i;
+        ok = mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns);
+        if (!ok) break;
+        if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kStageBytes);
           const uint32_t bar = full_leader + stage * 8;
           const int kt = kb * Kind<FMT>::kSfTiles;
@@ -204,26 +202,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(&tmSA, bar, sf, 0, (2 * mb + rank) * a.sf_tiles + kt);
           tma_load_2d_pair(&tmSB, bar, sf + Cfg::kSf, 0, 2 * nb * a.sf_tiles + kt);
           tma_load_2d_pair(&tmSB, bar, sf + 2 * Cfg::kSf, 0, (2 * nb + 1) * a.sf_tiles + kt);
-          armed |= 1u << stage;
-          parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        armed |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {
+    }
+    if (!ok) {
+      if (lane == 0)
         raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleProducer << 4) | 3);
-        if (leader) {
-          for (int s = 0; s < kStages; ++s)
-            if (armed & (1u << s))
-              (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
-        } else {
-          // this CTA's loads complete on the leader's barriers, which it cannot
-          // poll; give loads already issued ample time to land
-          spin_ns(2000000);
-        }
+      if (leader) {
+        for (int s = 0; s < kStages; ++s)
+          if (armed & (1u << s))
+            (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
+      } else {
+        // this CTA's loads complete on the leader's barriers, which it cannot
+        // poll; give loads already issued ample time to land
+        spin_ns(2000000);
       }
+      __syncwarp();
     }
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer (leader) ---

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(received + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform
   const int lane = threadIdx.x & 31;
   const int splits = static_cast<int>(cluster_size());
   const int rank = static_cast<int>(cluster_ctarank());
@@ -176,16 +176,16 @@ __global__ void __launch_bounds__(kThreads)
   grid_dependency_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, parity = 0;
-      bool ok = true;
-      const uint64_t policy = l2_policy_evict_first();
-      for (int s = s_begin; s < s_end; ++s) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns)) {
-          ok = false;
-          break;
-        }
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, parity = 0;
+    bool ok = true;
+    const uint64_t policy = l2_policy_evict_first();
+    const uint8_t* sb = a.SB + static_cast<int64_t>(nt) * a.tiles * kTileBytes;
+    const uint8_t* sa = a.SA + static_cast<int64_t>(m0 / kTileRows) * a.tiles * kTileBytes;
+    for (int s = s_begin; s < s_end; ++s) {
+      ok = mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns);
+      if (!ok) break;
+      if (elect_one()) {
         // the last stage may have one scale tile of two
         const int kt = s * kSfTiles;
         const uint32_t sf = static_cast<uint32_t>(min(kSfTiles, a.tiles - kt)) * kTileBytes;
@@ -197,24 +197,25 @@ __global__ void __launch_bounds__(kThreads)
           tma_load_2d(&tmB, &full[stage], w, s * kRowBytes, n0);
         tma_load_2d(&tmA, &full[stage], smX + stage * Cfg::kXBytes, s * kRowBytes, m0);
         uint8_t* sfw = smS + stage * 2 * Cfg::kSfBytes;
-        bulk_load(sfw, a.SB + (static_cast<int64_t>(nt) * a.tiles + kt) * kTileBytes, sf,
+        bulk_load(sfw, sb + static_cast<int64_t>(kt) * kTileBytes, sf, &full[stage]);
+        bulk_load(sfw + Cfg::kSfBytes, sa + static_cast<int64_t>(kt) * kTileBytes, sf,
                   &full[stage]);
-        bulk_load(sfw + Cfg::kSfBytes,
-                  a.SA + (static_cast<int64_t>(m0 / kTileRows) * a.tiles + kt) * kTileBytes, sf,
-                  &full[stage]);
-        armed |= 1u << stage;
-        parity = (parity & ~(1u << stage)) | (phase << stage);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      if (!ok) {
+      __syncwarp();
+      armed |= 1u << stage;
+      parity = (parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {
+      if (lane == 0)
         raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleProducer << 4) | 1);
-        // let every load already issued land before shared memory is released
-        for (int s = 0; s < kStages; ++s)
-          if (armed & (1u << s)) (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
-      }
+      // let every load already issued land before shared memory is released
+      for (int s = 0; s < kStages; ++s)
+        if (armed & (1u << s)) (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
+      __syncwarp();
     }
   } else if (warp == 1) {
     const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
@@ -231,10 +232,9 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t s_addr = smem_u32(smS + stage * 2 * Cfg::kSfBytes);
         const uint32_t sfw = base + Cfg::kSfBase + stage * 2 * Kind<FMT>::kSfCols;
         const uint32_t sfx = sfw + Kind<FMT>::kSfCols;
-        const int have = min(kSfTiles, a.tiles - s * kSfTiles);
+        // (a second tile that the last k-block does not have is copied and not used)
 #pragma unroll
         for (int t = 0; t < kSfTiles; ++t) {
-          if (t >= have) break;
           copy_scales<1>(sfw + 4 * t, (s_addr + t * kTileBytes) >> 4);
           copy_scales<1>(sfx + 4 * t, (s_addr + Cfg::kSfBytes + t * kTileBytes) >> 4);
         }

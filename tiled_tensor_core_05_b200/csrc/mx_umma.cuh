@@ -40,8 +40,8 @@ __host__ __device__ constexpr uint32_t mx_idesc(int m, int n, int k) {
 
 // The MMA warp runs its loop as a whole, so that descriptors and addresses stay
 // in uniform registers (a lane of its own would move every operand of every
-// instruction there: 404 instead of %%% us at 8192^3 MXFP8); one elected lane
-// issues.
+// instruction there: 225 instead of 204 us at 8192 x 14336 x 4096 MXFP4); one
+// elected lane issues.  So does the producer warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
