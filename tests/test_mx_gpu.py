@@ -254,7 +254,8 @@ def test_rms_norm_of_special_rows(fmt):
 SHAPES = [(1, 1, 1), (1, 128, 32), (2, 130, 33), (16, 128, 256), (17, 100, 100), (32, 777, 1000),
           (33, 64, 300), (64, 257, 129), (65, 128, 128), (128, 128, 512), (129, 300, 1025),
           (200, 1000, 700), (256, 256, 256), (300, 515, 2050), (513, 257, 130), (1, 1000, 8192),
-          (40, 130, 16385)]
+          (40, 130, 16385), (65, 257, 4100), (70, 600, 4100), (129, 100, 5000),
+          (200, 1000, 8200), (385, 514, 4097)]
 
 
 # enough 256 x 256 tiles for the CTA-pair kernel: one wave and several, ragged
@@ -302,7 +303,8 @@ def random_operand(rng, rows, cols, fmt, scale):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 300, 700), (20, 200, 1000), (50, 129, 515), (100, 128, 2000),
-                                   (300, 400, 1100), (1601, 1500, 640)])
+                                   (300, 400, 1100), (150, 300, 4200),
+                                   (1601, 1500, 640)])
 @pytest.mark.parametrize("fmt", ref.FORMATS)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("act", ["none", "relu", "gelu"])

@@ -29,7 +29,8 @@ BIND = os.path.join(PKG, "_mxbind.so")  # CPython binding of libttcmx, against t
 BIND_SOURCE = "mx_bind.cpp"
 COMMON = ["host_common.cu"]  # linked into both libraries
 SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu"]
-MX_SOURCES = ["mx_api.cu", "mx_rows.cu", "mx_gemm_split.cu", "mx_gemm_pair.cu"]
+MX_SOURCES = ["mx_api.cu", "mx_rows.cu", "mx_gemm_split.cu", "mx_gemm_pair.cu",
+              "mx_gemm_pair_split.cu"]
 HEADERS = ["sm100.cuh", "internal.h", "skinny_common.cuh", "tile_common.cuh", "mx_internal.h", "mx_common.cuh",
            "mx_umma.cuh"]
 

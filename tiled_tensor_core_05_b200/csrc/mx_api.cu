@@ -96,17 +96,26 @@ int run_gemm(const MxGemmProblem& p) {
   rc = check_mx(p.A, p.SA, p.M, p.K, p.lda, p.format, d.device);
   if (rc == GEMM_OK) rc = check_mx(p.B, p.SB, p.N, p.K, p.ldb, p.format, d.device);
   if (rc != GEMM_OK) return rc;
-  // The pair kernel's 256 x 256 tiles read half the bytes per product that the
-  // split kernel's 64 x 128 ones do, but need enough tiles, with most of their
-  // rows, to keep the SMs busy.  Measured: 1500 x 2000 x 2000 MXFP4 (48 pair
-  // tiles) 9.1 us as pairs, 13.3 split; 256 x 9000 x 4096 (36) 14.4 and 13.6; 128 x
-  // 18944 x 4096 (74, half empty; one wave of the split kernel) 15.9 and 14.8;
-  // 100 x 28672 x 8192 (112; two waves) 37.4 and 40.4.
+  // Measured (us: split kernel, pair kernel, pair tiles with K divided):
+  //   1500 x 2000 x 2000 MXFP4 (48 tiles of 256 x 256)   17.9   8.7  16.9
+  //   1024 x 4096 x 8192 MXFP8 (64)                      49.0  27.8  42.0
+  //   256 x 9000 x 4096 MXFP8 (36)                       17.0  17.1  15.3
+  //   256 x 4096 x 8192 MXFP8 (16)                       17.4  24.5  15.7
+  //   512 x 2048 x 2048 MXFP4 (16; 8 k-blocks)            7.9   7.6   8.2
+  //   128 x 18944 x 4096 MXFP4 (74, half empty)          13.7  14.0  14.1
+  //   100 x 28672 x 8192 MXFP4 (112; two waves split)    34.2  29.2  32.1
+  // So: the pair kernel where its tiles fill half the SMs, if they are not half
+  // empty (M > 128) or the split kernel's would take two waves;
+  // else K divided among pairs from 65 rows and 16 k-blocks on; else the split
+  // kernel.
   const int64_t pair_tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
   const int64_t split_tiles = ((p.M + 63) / 64) * ((p.N + 127) / 128);
-  const bool pairs = p.M > 64 && pair_tiles >= d.sm_count / 4 &&
-                     (p.M > 128 || split_tiles > 2 * d.sm_count);
-  return pairs ? launch_mx_pair_gemm(p, d) : launch_mx_split_gemm(p, d);
+  const int64_t num_kb = (mx_row_bytes(p.K, p.format) + 127) / 128;
+  if (p.M > 64 && pair_tiles >= d.sm_count / 4 &&
+      (p.M > 128 || split_tiles > 2 * d.sm_count))
+    return launch_mx_pair_gemm(p, d);
+  if (p.M > 64 && num_kb >= 16) return launch_mx_pair_split_gemm(p, d);
+  return launch_mx_split_gemm(p, d);
 }
 
 }  // namespace

@@ -63,16 +63,12 @@ struct SplitCfg {
 
 struct SplitArgs {
   const uint8_t *SB, *SA;
-  const uint16_t* bias;
-  uint16_t* C;
-  int64_t ldc;
-  int M, N;
+  Output out;
   int row_bytes;  // bytes of a row of elements
   int tiles;      // scale tiles along K
   int stages;     // ring stages along K
   int tiles_m;
   int stream_b;   // B is read once: let L2 drop it first
-  int dtype, act;
   int* status;
   uint64_t timeout_ns;
 };
@@ -84,35 +80,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-
-__device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float4& y) {
-  v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-  v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-}
-
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-  return r;
-}
-
-// Eight columns of a row of C from their fp32 sums: bias, activation, one
-// rounding, stored as 16 bytes or, across the edge, one by one.
-template <class T>
-__device__ __forceinline__ void store_row8(const SplitArgs& a, int m, int n, const float (&v)[8]) {
-  const int count = min(8, a.N - n);
-  uint4 bias = make_uint4(0, 0, 0, 0);
-  if (a.bias != nullptr) bias = load8(a.bias + n, count);
-  float b[8], y[8];
-  unpack8<T>(bias, b);
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 r = finish2(make_float2(v[i], v[i + 1]), make_float2(b[i], b[i + 1]), a.act);
-    y[i] = r.x;
-    y[i + 1] = r.y;
-  }
-  store8(a.C + static_cast<int64_t>(m) * a.ldc + n, pack8<T>(y), count);
 }
 
 template <int FMT, int BN>
@@ -142,7 +109,7 @@ __global__ void __launch_bounds__(kThreads)
   const int tile = static_cast<int>(blockIdx.x) / splits;
   const int mt = tile % a.tiles_m, nt = tile / a.tiles_m;
   const int m0 = mt * BN, n0 = nt * kTileN;
-  const int rows = min(BN, a.M - m0);
+  const int rows = min(BN, a.out.M - m0);
   const int s_begin = static_cast<int>(static_cast<int64_t>(a.stages) * rank / splits);
   const int s_end = static_cast<int>(static_cast<int64_t>(a.stages) * (rank + 1) / splits);
 
@@ -309,30 +276,24 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
   }
 
-  auto store = [&](int m, int n, const float (&v)[8]) {
-    if (a.dtype == MX_F16)
-      store_row8<__half>(a, m, n, v);
-    else
-      store_row8<__nv_bfloat16>(a, m, n, v);
-  };
   if (*abort_flag == 0 && splits > 1 && pull) {
     // items: 8 columns of a row, dealt out over the threads of the cluster
     for (int it = rank * kThreads + threadIdx.x; it < rows * (kTileN / 8); it += splits * kThreads) {
       const int m = it >> 4, c = (it & 15) * 8;
-      if (n0 + c >= a.N) continue;
+      if (n0 + c >= a.out.N) continue;
       float v[8] = {};
       for (int s = 0; s < splits; ++s) {
         const uint32_t src = map_to_cta(
             smem_u32(smem) + static_cast<uint32_t>(m * kTileN + c) * 4, static_cast<uint32_t>(s));
         add8(v, ld_cluster_f4(src), ld_cluster_f4(src + 16));
       }
-      store(m0 + m, n0 + c, v);
+      store_row8(a.out, m0 + m, n0 + c, v);
     }
   } else if (*abort_flag == 0) {
     // items: 8 columns of one of this CTA's rows
     for (int it = threadIdx.x; it < (r1 - r0) * (kTileN / 8); it += kThreads) {
       const int m = it >> 4, c = (it & 15) * 8;
-      if (n0 + c >= a.N) continue;
+      if (n0 + c >= a.out.N) continue;
       float v[8] = {};
       for (int s = 0; s < splits; ++s) {
         const uint8_t* base = s == rank ? smem + r0 * kTileN * 4
@@ -340,7 +301,7 @@ __global__ void __launch_bounds__(kThreads)
         const float4* src = reinterpret_cast<const float4*>(base) + (m * kTileN + c) / 4;
         add8(v, src[0], src[1]);
       }
-      store(m0 + r0 + m, n0 + c, v);
+      store_row8(a.out, m0 + r0 + m, n0 + c, v);
     }
   }
   __syncwarp();
@@ -355,12 +316,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Clusters of c = 1 .. 8 CTAs that the GPU holds at one CTA an SM (0 = not
-// asked yet, per device; the GPCs leave SMs over).
-struct Residency {
-  std::atomic<int> clusters[9] = {};
-};
-
 // Into how many parts of at least four k-blocks K is divided: as many as run in
 // one wave, since a second wave costs more than the division brings (32 x 8192
 // x 4096 MXFP8, 64 tiles: 1 part 15.8 us, 2 parts 11.5, 4 parts 10.2, 5 parts 16.2).
@@ -370,20 +325,8 @@ int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   static Residency residency[64];
   int splits = 1;
   for (int c = 2; c <= 8 && stages >= 4 * c; ++c) {
-    std::atomic<int>& known = residency[d.device & 63].clusters[c];
-    int n = known.load(std::memory_order_relaxed);
-    if (n == 0) {
-      Launch l(dim3(static_cast<unsigned>(c * d.sm_count)), dim3(kThreads), Cfg::kSmemBytes,
-               nullptr);
-      l.cluster(static_cast<unsigned>(c));
-      if (cudaOccupancyMaxActiveClusters(&n, split_gemm_kernel<FMT, BN>, &l.cfg) !=
-              cudaSuccess ||
-          n <= 0) {
-        cudaGetLastError();
-        n = d.sm_count / (c + 1);
-      }
-      known.store(n, std::memory_order_relaxed);
-    }
+    const int n = residency[d.device & 63].of(c, split_gemm_kernel<FMT, BN>, kThreads,
+                                              Cfg::kSmemBytes, d);
     if (tiles <= static_cast<int64_t>(n) * Cfg::kPerSm) splits = c;
   }
   return splits;
@@ -424,18 +367,12 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
   if (tiles * splits > INT32_MAX) return GEMM_ERR_INVALID_ARG;
   const SplitArgs a{static_cast<const uint8_t*>(p.SB),
                     static_cast<const uint8_t*>(p.SA),
-                    static_cast<const uint16_t*>(p.bias),
-                    static_cast<uint16_t*>(p.C),
-                    p.ldc,
-                    static_cast<int>(p.M),
-                    static_cast<int>(p.N),
+                    output_of(p),
                     static_cast<int>(row_bytes),
                     static_cast<int>(scale_tiles(p.K)),
                     static_cast<int>(stages),
                     static_cast<int>(tiles_m),
                     tiles_m == 1,
-                    p.dtype,
-                    p.act,
                     d.status,
                     d.timeout_ns};
   Launch l(dim3(static_cast<unsigned>(tiles * splits)), dim3(kThreads), Cfg::kSmemBytes, p.stream);

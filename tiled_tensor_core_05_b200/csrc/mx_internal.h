@@ -1,6 +1,8 @@
 // Host-side declarations shared by the translation units of libttcmx.
 #pragma once
 
+#include <atomic>
+
 #include "../../include/gemm_mx.h"
 #include "internal.h"
 
@@ -39,6 +41,7 @@ int launch_dequantize(const ConvertProblem& p);
 int launch_rms_norm(const NormProblem& p);
 int launch_mx_split_gemm(const MxGemmProblem& p, const DeviceCtx& d);
 int launch_mx_pair_gemm(const MxGemmProblem& p, const DeviceCtx& d);
+int launch_mx_pair_split_gemm(const MxGemmProblem& p, const DeviceCtx& d);
 // C = act(bias), or act(0) without one: a product over no elements.
 int launch_mx_bias_fill(const MxGemmProblem& p);
 
@@ -60,6 +63,27 @@ struct Launch {
     a.val.clusterDim.x = n;
     a.val.clusterDim.y = 1;
     a.val.clusterDim.z = 1;
+  }
+};
+
+// How many clusters of c CTAs (c = 2 .. 8) of a kernel the GPU holds at one CTA
+// an SM, asked once per device: the GPCs leave SMs over.
+struct Residency {
+  std::atomic<int> clusters[9] = {};  // 0 = not asked yet
+  template <class K>
+  int of(int c, K kern, int threads, size_t smem, const DeviceCtx& d) {
+    int n = clusters[c].load(std::memory_order_relaxed);
+    if (n == 0) {
+      Launch l(dim3(static_cast<unsigned>(c * d.sm_count)), dim3(static_cast<unsigned>(threads)),
+               smem, nullptr);
+      l.cluster(static_cast<unsigned>(c));
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &l.cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = d.sm_count / (c + 1);
+      }
+      clusters[c].store(n, std::memory_order_relaxed);
+    }
+    return n;
   }
 };
 

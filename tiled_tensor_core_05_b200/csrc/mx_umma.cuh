@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "mx_common.cuh"
+#include "mx_internal.h"
 
 namespace ttc {
 namespace mx {
@@ -160,6 +161,56 @@ __device__ __forceinline__ float2 finish2(float2 v, float2 b, int act) {
   return act == kActRelu   ? activate2<kActRelu>(v)
          : act == kActGelu ? activate2<kActGelu>(v)
                            : v;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float4& y) {
+  v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+  v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+}
+
+// What the epilogues of the kernels that divide K need of C.
+struct Output {
+  uint16_t* C;
+  const uint16_t* bias;
+  int64_t ldc;
+  int M, N;
+  int dtype, act;
+};
+
+inline Output output_of(const MxGemmProblem& p) {
+  return Output{static_cast<uint16_t*>(p.C), static_cast<const uint16_t*>(p.bias), p.ldc,
+                static_cast<int>(p.M),       static_cast<int>(p.N),             p.dtype, p.act};
+}
+
+// Eight columns of a row of C from their fp32 sums: bias, activation, one
+// rounding, stored as 16 bytes or, across the edge, one by one.
+template <class T>
+__device__ __forceinline__ void store_row8(const Output& o, int m, int n, const float (&v)[8]) {
+  const int count = min(8, o.N - n);
+  uint4 bias = make_uint4(0, 0, 0, 0);
+  if (o.bias != nullptr) bias = load8(o.bias + n, count);
+  float b[8], y[8];
+  unpack8<T>(bias, b);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 r = finish2(make_float2(v[i], v[i + 1]), make_float2(b[i], b[i + 1]), o.act);
+    y[i] = r.x;
+    y[i + 1] = r.y;
+  }
+  store8(o.C + static_cast<int64_t>(m) * o.ldc + n, pack8<T>(y), count);
+}
+
+__device__ __forceinline__ void store_row8(const Output& o, int m, int n, const float (&v)[8]) {
+  if (o.dtype == MX_F16)
+    store_row8<__half>(o, m, n, v);
+  else
+    store_row8<__nv_bfloat16>(o, m, n, v);
 }
 
 }  // namespace mx
