@@ -34,9 +34,10 @@ constexpr int kTileN = 128;  // columns of C per tile
 
 constexpr int kPullRows = 4;  // up to so many rows the parts are read, not sent
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool DEEP>
 struct SplitCfg {
-  static constexpr int kStages = BN == 64 ? 4 : 5;  // two CTAs an SM
+  // one CTA an SM with a deep ring, or two
+  static constexpr int kStages = DEEP ? (BN == 16 ? 10 : BN == 32 ? 9 : 8) : (BN == 64 ? 4 : 5);
   static constexpr int kWBytes = kTileN * kRowBytes;
   static constexpr int kXBytes = BN * kRowBytes;
   static constexpr int kSfBytes = Kind<FMT>::kSfTiles * kTileBytes;
@@ -82,11 +83,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool DEEP>
 __global__ void __launch_bounds__(kThreads)
     split_gemm_kernel(const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmA, const SplitArgs a) {
-  using Cfg = SplitCfg<FMT, BN>;
+  using Cfg = SplitCfg<FMT, BN, DEEP>;
   constexpr int kStages = Cfg::kStages;
   constexpr int kSfTiles = Kind<FMT>::kSfTiles;
   extern __shared__ uint8_t smem_raw[];
@@ -319,24 +320,24 @@ __global__ void __launch_bounds__(kThreads)
 // Into how many parts of at least four k-blocks K is divided: as many as run in
 // one wave, since a second wave costs more than the division brings (32 x 8192
 // x 4096 MXFP8, 64 tiles: 1 part 15.8 us, 2 parts 11.5, 4 parts 10.2, 5 parts 16.2).
-template <int FMT, int BN>
+template <int FMT, int BN, bool DEEP>
 int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
-  using Cfg = SplitCfg<FMT, BN>;
+  using Cfg = SplitCfg<FMT, BN, DEEP>;
   static Residency residency[64];
   int splits = 1;
   for (int c = 2; c <= 8 && stages >= 4 * c; ++c) {
-    const int n = residency[d.device & 63].of(c, split_gemm_kernel<FMT, BN>, kThreads,
+    const int n = residency[d.device & 63].of(c, split_gemm_kernel<FMT, BN, DEEP>, kThreads,
                                               Cfg::kSmemBytes, d);
     if (tiles <= static_cast<int64_t>(n) * Cfg::kPerSm) splits = c;
   }
   return splits;
 }
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool DEEP>
 bool set_attributes(const DeviceCtx& d) {
   static std::atomic<uint64_t> attr_done{0};
-  auto kern = split_gemm_kernel<FMT, BN>;
-  using Cfg = SplitCfg<FMT, BN>;
+  auto kern = split_gemm_kernel<FMT, BN, DEEP>;
+  using Cfg = SplitCfg<FMT, BN, DEEP>;
   const uint64_t bit = 1ull << (d.device & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -352,10 +353,10 @@ bool set_attributes(const DeviceCtx& d) {
   return true;
 }
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool DEEP>
 int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
-  using Cfg = SplitCfg<FMT, BN>;
-  auto kern = split_gemm_kernel<FMT, BN>;
+  using Cfg = SplitCfg<FMT, BN, DEEP>;
+  auto kern = split_gemm_kernel<FMT, BN, DEEP>;
   const int64_t row_bytes = mx_row_bytes(p.K, FMT);
   CUtensorMap tB, tA;
   int rc = encode_tmap_u8_2d(&tB, p.B, row_bytes, p.N, p.ldb, kTileN);
@@ -381,12 +382,22 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
+template <int FMT, int BN, bool DEEP>
+int launch_depth(const MxGemmProblem& p, const DeviceCtx& d, int64_t tiles) {
+  if (!set_attributes<FMT, BN, DEEP>(d)) return GEMM_ERR_LAUNCH;
+  const int64_t stages = (mx_row_bytes(p.K, FMT) + kRowBytes - 1) / kRowBytes;
+  return launch<FMT, BN, DEEP>(p, d, choose_splits<FMT, BN, DEEP>(tiles, stages, d));
+}
+
+// Where the tiles alone give most SMs one CTA, one with a deep ring and the
+// whole of K; else two an SM, which also cover each other's ends (32 x 14336 x
+// 4096 MXFP8, 112 tiles: 12.7 us, 14.0 with two; 32 x 28672 x 8192 MXFP4, 224
+// tiles: 26.6 us, 22.2 with two).
 template <int FMT, int BN>
 int launch_tile(const MxGemmProblem& p, const DeviceCtx& d) {
-  if (!set_attributes<FMT, BN>(d)) return GEMM_ERR_LAUNCH;
   const int64_t tiles = (p.M + BN - 1) / BN * ((p.N + kTileN - 1) / kTileN);
-  const int64_t stages = (mx_row_bytes(p.K, FMT) + kRowBytes - 1) / kRowBytes;
-  return launch<FMT, BN>(p, d, choose_splits<FMT, BN>(tiles, stages, d));
+  return tiles > d.sm_count / 2 && tiles <= d.sm_count ? launch_depth<FMT, BN, true>(p, d, tiles)
+                                                       : launch_depth<FMT, BN, false>(p, d, tiles);
 }
 
 template <int FMT>
