@@ -93,8 +93,9 @@ GEMM_API int mx_dequantize(const void* Q, const void* S, void* X, int64_t rows, 
  * X, R, H: rows x cols of type dtype, W: cols values of type dtype, 16-byte
  * aligned.  H may be X or R itself (the stream updated in place), and Y with
  * MX_NONE may be X itself when R is NULL.  The mean is taken over the exact
- * squares; every output is y correctly rounded (to about 2^-45 beside a tie).
- * (The squares are held in fp32: |h| up to 1.8e19.)  eps >= 0. */
+ * squares; every output is y correctly rounded (to about 2^-43 beside a tie).
+ * (h^2 and h * W are held in fp32: |h| and |h * W| up to 1.8e19, and from
+ * about 1e-16 for that precision.)  eps >= 0. */
 GEMM_API int mx_rms_norm(const void* X, const void* R, const void* W, void* H, void* Y, void* S,
                          int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, int64_t ldh,
                          int64_t ldy, float eps, int dtype, int format, gemm_stream_t stream);

@@ -18,9 +18,16 @@
 //     0..255, buffer 1 ends where the scales begin.  Every epilogue warp takes
 //     all its 64 columns into registers at once and then hands them back, so
 //     the next tile's MMAs wait for the reads of a tile, not for its epilogue.
-//   * 16 epilogue warps: the GELU epilogue is about 21 instructions and two
-//     special-function results an element, nearly as long as the MMAs of a
-//     4-bit tile with K = 4096; with 8 warps it was not hidden.
+//   * 16 epilogue warps, 64 columns each: the GELU epilogue is about 21
+//     instructions and two special-function results an element, nearly as long
+//     as the MMAs of a 4-bit tile with K = 4096.
+//
+// Measured: 8192^3 MXFP8 + ReLU 369 us (2.98 PFLOP/s, the tensor pipe active for
+// 90 % of the cycles; 444 us back to back under the power cap), 8192 x 14336 x
+// 4096 MXFP4 + bias + GELU 190 us (5.07 PFLOP/s), without an epilogue to speak
+// of and K = 16384 590 us (6.52 PFLOP/s).  A 4-bit k-block takes 346 ns, of which
+// the 4 MMAs 270 and the 6 scale copies the rest; a tile costs 1.5 us besides
+// (handing over the shared columns 0.6, the stores 0.9), 2.2 with GELU.
 #include "mx_internal.h"
 #include "mx_umma.cuh"
 #include "tile_common.cuh"

@@ -9,10 +9,14 @@
 // shared memories each), and adds the parts of its own rows in rank order.
 // Nothing is kept in device memory between or during calls (no workspace, no
 // counters), and the order of the sums is fixed by the shape.  Reading the
-// other CTAs' parts with loads instead runs at some 8 bytes a clock and SM (2 us
-// for 64 x 128 parts of two CTAs); it is done only for a few rows, where the
-// wait for the copies would cost more (1 x 8192 x 4096 MXFP4: 7.1 us, 7.6 with
-// copies; 16 x 2048 x 8192: 7.8 us, 6.8 with copies).
+// other CTAs' parts with loads instead runs at some 8 bytes a clock and SM (60 x
+// 4096 x 8192 MXFP8: 15.0 us, 11.6 with copies; 16 x 2048 x 8192: 7.6 and 7.0);
+// it is done only for a few rows, where waiting for the copies costs more (1 x
+// 8192 x 4096 MXFP8: 8.6 us, 9.2 with copies).
+//
+// Bound by reading B from device memory where it is large (32 x 28672 x 8192
+// MXFP4: 22.1 us, 5.7 TB/s; 1 x 28672 x 4096 MXFP8: 20.5 us, 5.8 TB/s), else by a
+// chain of about 6 us: launch, first load, accumulator, joining, store.
 //
 //   warp 0   TMA producer: elements by tensor maps into 128-byte-swizzled
 //            shared memory, scale tiles by plain bulk copies
@@ -31,7 +35,6 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kTileN = 128;  // columns of C per tile
-
 constexpr int kPullRows = 4;  // up to so many rows the parts are read, not sent
 
 template <int FMT, int BN, bool DEEP>
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // Into how many parts of at least four k-blocks K is divided: as many as run in
 // one wave, since a second wave costs more than the division brings (32 x 8192
-// x 4096 MXFP8, 64 tiles: 1 part 15.8 us, 2 parts 11.5, 4 parts 10.2, 5 parts 16.2).
+// x 4096 MXFP8, 64 tiles: 1 part 11.7 us, 2 parts 10.5, 4 parts 10.0, 5 parts 15.1).
 template <int FMT, int BN, bool DEEP>
 int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   using Cfg = SplitCfg<FMT, BN, DEEP>;

