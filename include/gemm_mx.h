@@ -42,7 +42,8 @@
  * mx_get_device_status().  No entry point throws, allocates device memory or
  * keeps a reference to its arguments, so calls on several streams or host
  * threads share nothing, and every call can be captured in a CUDA graph (make
- * one call outside a capture first: it looks up the device).  Outputs must
+ * one such call outside a capture first: it looks up the device and sets up the
+ * kernel).  Outputs must
  * not overlap inputs unless an entry point says so.
  */
 #ifndef TTCMX_GEMM_MX_H

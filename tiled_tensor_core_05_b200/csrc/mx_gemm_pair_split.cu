@@ -228,10 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();            // all parts are written, all rings free
   uint8_t* incoming = smem + C::kPartBytes;
   if (parts > 1) {
-    if (threadIdx.x == 0 && *abort_flag == 0) {
+    if (threadIdx.x == 0) {
       mbar_arrive_expect_tx(received,
                             static_cast<uint32_t>((parts - 1) * (r1 - r0) * kHalfN * 4));
-      for (int k = 1; k < parts; ++k) {
+      for (int k = 1; k < parts && *abort_flag == 0; ++k) {
         const int to = part + k < parts ? part + k : part + k - parts;
         const int from_row = first_row(to), n = first_row(to + 1) - from_row;
         if (n == 0) continue;
@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   map_to_cta(smem_u32(received), cta));
       }
     }
-    if (r1 > r0 && *abort_flag == 0 && !mbar_wait(received, 0, abort_flag, a.timeout_ns))
+    // (after an abort, too: what others have sent has to land before this CTA ends)
+    if (r1 > r0 && !mbar_wait(received, 0, nullptr, a.timeout_ns))
       raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 2);
   }
   if (*abort_flag == 0) {

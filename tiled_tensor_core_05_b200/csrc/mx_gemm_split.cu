@@ -259,10 +259,10 @@ __global__ void __launch_bounds__(kThreads)
   if (splits > 1) {
     fence_proxy_async_smem();  // the part is read by bulk copies
     cluster_sync();            // all parts are written, all rings free
-    if (!pull && threadIdx.x == 0 && *abort_flag == 0) {
+    if (!pull && threadIdx.x == 0) {
       mbar_arrive_expect_tx(received,
                             static_cast<uint32_t>((splits - 1) * (r1 - r0) * kTileN * 4));
-      for (int k = 1; k < splits; ++k) {
+      for (int k = 1; k < splits && *abort_flag == 0; ++k) {
         const int to = rank + k < splits ? rank + k : rank + k - splits;
         const int from_row = first_row(to), n = first_row(to + 1) - from_row;
         if (n == 0) continue;
@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(kThreads)
                   map_to_cta(smem_u32(received), static_cast<uint32_t>(to)));
       }
     }
-    if (!pull && r1 > r0 && *abort_flag == 0 && !mbar_wait(received, 0, abort_flag, a.timeout_ns))
+    // (after an abort, too: what others have sent has to land before this CTA ends)
+    if (!pull && r1 > r0 && !mbar_wait(received, 0, nullptr, a.timeout_ns))
       raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 2);
   } else {
     __syncthreads();
