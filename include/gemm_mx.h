@@ -95,8 +95,9 @@ GEMM_API int mx_dequantize(const void* Q, const void* S, void* X, int64_t rows, 
  * aligned.  H may be X or R itself (the stream updated in place), and Y with
  * MX_NONE may be X itself when R is NULL.  The mean is taken over the exact
  * squares; every output is y correctly rounded (to about 2^-43 beside a tie).
- * (h^2 and h * W are held in fp32: |h| and |h * W| up to 1.8e19, and from
- * about 1e-16 for that precision.)  eps >= 0. */
+ * (h * W is held in fp32, with h times 2^80 or 2^-80 in rows whose squares leave
+ * fp32's range: so scaled, |h * W| up to 3e38, and from about 1e-31 for that
+ * precision.)  eps >= 0. */
 GEMM_API int mx_rms_norm(const void* X, const void* R, const void* W, void* H, void* Y, void* S,
                          int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, int64_t ldh,
                          int64_t ldy, float eps, int dtype, int format, gemm_stream_t stream);

@@ -249,6 +249,34 @@ def test_rms_norm_of_special_rows(fmt):
         assert np.array_equal(data, ref.pack(codes, fmt))
 
 
+@pytest.mark.parametrize("rows_of_ten", [1, 30])
+@pytest.mark.parametrize("cols", [100, 3000, 40000])
+@pytest.mark.parametrize("fmt", [None, "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_rms_norm_where_squares_leave_fp32(rows_of_ten, cols, fmt, eps):
+    """bf16 rows from its smallest values to its largest, beside ordinary ones."""
+    t = torch.bfloat16
+    rng = np.random.default_rng(cols)
+    # (with eps = 1e-6 an h this small is not scaled: kept where h w is normal in fp32)
+    size = np.exp2([-131.0 if eps == 0 else -90, -80, -75, -60, -41, 0, 40, 63, 64, 125])
+    size = np.tile(size, rows_of_ten)[:, None]
+    x = host16(np.clip(rng.standard_normal((len(size), cols)), -3.9, 3.9) * size, t)
+    r = host16(np.clip(rng.standard_normal((len(size), cols)), -3.9, 3.9) * size, t)
+    w = host16(1 + 0.1 * rng.standard_normal(cols), t)
+    h = ref.round_to(x + r, t)
+    assert np.isfinite(h).all() and (np.abs(h).max(1) > 0).all()
+    want = ref.norm(h, w, float(np.float32(eps)))
+    got, hh = ttc.rms_norm(dev16(x, t), dev_vec(w, t), eps, residual=dev16(r, t), format=fmt)
+    assert np.array_equal(ref.to_np(hh), h)
+    if fmt is None:
+        assert np.array_equal(ref.to_np(got), ref.round_to(want, t))
+    else:
+        codes, scales = ref.quantize(want, fmt)
+        assert np.array_equal(got.scales.cpu().numpy(), ref.tile_scales(scales, cols))
+        data = got.data.cpu().numpy()[:, :ref.row_bytes(cols, fmt)]
+        assert np.array_equal(data, ref.pack(codes, fmt))
+
+
 # --------------------------------------------------------------------- the product ---
 
 SHAPES = [(1, 1, 1), (1, 128, 32), (2, 130, 33), (16, 128, 256), (17, 100, 100), (32, 777, 1000),

@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(kTileThreads)
 //
 // Precision: an MX element is decided by rounding at half steps, where the
 // last bits of y matter.  h^2 and h w are exact in fp32 (products of two
-// 16-bit values); the squares are summed with their rounding errors (two-sum)
+// 16-bit values; a row of bf16 whose squares leave fp32's range is taken times
+// a power of two, which costs the other rows nothing measurable); the squares are summed with their rounding errors (two-sum)
 // and then in fp64; s is held as two fp32 numbers.  y in fp32 is on the same
 // side of every value halfway between two outputs as the exact y, unless it
 // lies on such a value itself, which its low bits show; only then is it
@@ -267,10 +268,24 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
   uint16_t* h = a.H != nullptr ? a.H + row * a.ldh : nullptr;
   uint4 hv[V > 0 ? V : 1];
   float2 acc = make_float2(0.0f, 0.0f), err = make_float2(0.0f, 0.0f);
+  // h is taken times c, a power of two: 1, unless the row's squares leave fp32's
+  // range, which bf16 values can
+  constexpr bool kWide = std::is_same<T, __nv_bfloat16>::value;
+  float c = 1.0f;
+  auto values = [&](uint32_t w) {
+    const float2 v = unpack2<T>(w);
+    return kWide && c != 1.0f ? __fmul2_rn(v, splat2(c)) : v;
+  };
   auto squares = [&](const uint4& v) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) add_square(acc, err, unpack2<T>(w[k]));
+    for (int k = 0; k < 4; ++k) add_square(acc, err, values(w[k]));
+  };
+  // vector i of h once it has been stored, when there is no register copy
+  auto again = [&](int i) {
+    if (r != nullptr && h != nullptr) return load(h, i);  // written by this thread
+    const uint4 u = load(x, i);
+    return r != nullptr ? add8<T>(u, load(r, i)) : u;
   };
   if constexpr (V > 0) {
 #pragma unroll
@@ -311,22 +326,40 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
         *reinterpret_cast<uint32_t*>(a.S + scale_word(first + have + w / nt, w % nt, tiles)) = 0;
     }
   }
-  // an infinite sum has no rounding error (inf - inf is not one)
-  double sum = (isinf(acc.x) || isinf(acc.y))
-                   ? static_cast<double>(acc.x) + static_cast<double>(acc.y)
-                   : (static_cast<double>(acc.x) + static_cast<double>(acc.y)) +
-                         (static_cast<double>(err.x) + static_cast<double>(err.y));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const int wpr = tpr >> 5;
-  if (wpr > 1) {
-    double* mine = part + threadIdx.y * wpr;
-    if (lane == 0) mine[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    sum = 0.0;
-    for (int w = 0; w < wpr; ++w) sum += mine[w];
+  // mean of the squares + eps, of h c
+  auto mean = [&]() {
+    // an infinite sum has no rounding error (inf - inf is not one)
+    double sum = (isinf(acc.x) || isinf(acc.y))
+                     ? static_cast<double>(acc.x) + static_cast<double>(acc.y)
+                     : (static_cast<double>(acc.x) + static_cast<double>(acc.y)) +
+                           (static_cast<double>(err.x) + static_cast<double>(err.y));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (wpr > 1) {
+      double* mine = part + threadIdx.y * wpr;
+      if (lane == 0) mine[threadIdx.x >> 5] = sum;
+      __syncthreads();
+      sum = 0.0;
+      for (int w = 0; w < wpr; ++w) sum += mine[w];
+    }
+    return fma(sum, a.inv_cols, static_cast<double>(a.eps) * c * c);
+  };
+  double m = mean();
+  if (kWide && !(m > 0x1p-80 && m < 0x1p127)) {  // the same for all threads of the row
+    // 2^80 takes bf16's smallest value to 2^-53, 2^-80 its largest to 2^48
+    c = m < 1.0 ? 0x1p80f : 0x1p-80f;
+    acc = err = make_float2(0.0f, 0.0f);
+    if (wpr > 1) __syncthreads();  // the parts have been read
+    if constexpr (V > 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) squares(hv[v]);
+    } else {
+      for (int v = 0; v < steps; ++v) squares(again(threadIdx.x + v * tpr));
+    }
+    m = mean();
   }
-  const double s = inverse_sqrt(fma(sum, a.inv_cols, static_cast<double>(a.eps)));
+  const double s = inverse_sqrt(m);
   const float sh = static_cast<float>(s);
   const float sl = static_cast<float>(s - static_cast<double>(sh));
 
@@ -339,7 +372,7 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
     uint32_t low = ~0u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      p[k] = __fmul2_rn(unpack2<T>(hw[k]), unpack2<T>(ww[k]));
+      p[k] = __fmul2_rn(values(hw[k]), unpack2<T>(ww[k]));
       const float2 y = __ffma2_rn(p[k], splat2(sh), __fmul2_rn(p[k], splat2(sl)));
       low = min(low, min(__float_as_uint(y.x) & kTieMask<T, FMT>,
                          __float_as_uint(y.y) & kTieMask<T, FMT>));
@@ -378,14 +411,7 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
   } else {
     for (int v = 0; v < steps; ++v) {
       const int i = threadIdx.x + v * tpr;
-      uint4 u;
-      if (r != nullptr && h != nullptr) {
-        u = load(h, i);  // written by this thread above
-      } else {
-        u = load(x, i);
-        if (r != nullptr) u = add8<T>(u, load(r, i));
-      }
-      emit(i, u);
+      emit(i, again(i));
     }
   }
 }
