@@ -398,7 +398,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
                    d.status,
                    d.timeout_ns};
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tA, tB, tSA, tSB, a);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return launched(e);
 }
 
 template <int FMT, class T>

@@ -305,7 +305,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
                d.status,
                d.timeout_ns};
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tB, tA, tSB, tSA, a);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return launched(e);
 }
 
 }  // namespace

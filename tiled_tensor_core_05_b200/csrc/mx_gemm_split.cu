@@ -383,7 +383,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
   Launch l(dim3(static_cast<unsigned>(tiles * splits)), dim3(kThreads), Cfg::kSmemBytes, p.stream);
   l.cluster(static_cast<unsigned>(splits));
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tB, tA, a);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return launched(e);
 }
 
 template <int FMT, int BN, bool DEEP>
@@ -442,7 +442,7 @@ int launch_mx_bias_fill(const MxGemmProblem& p) {
                                           : cudaLaunchKernelEx(&l.cfg,
                                                                bias_fill_kernel<__nv_bfloat16>, c,
                                                                b, p.M, p.N, p.ldc, p.act);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return launched(e);
 }
 
 }  // namespace mx

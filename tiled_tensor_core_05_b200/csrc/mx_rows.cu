@@ -141,14 +141,15 @@ __global__ void __launch_bounds__(kTileThreads)
 // Precision: an MX element is decided by rounding at half steps, where the
 // last bits of y matter.  h^2 and h w are exact in fp32 (products of two
 // 16-bit values; a row of bf16 whose squares leave fp32's range is taken times
-// a power of two, which costs the other rows nothing measurable); the squares are summed with their rounding errors (two-sum)
-// and then in fp64; s is held as two fp32 numbers.  y in fp32 is on the same
-// side of every value halfway between two outputs as the exact y, unless it
-// lies on such a value itself, which its low bits show; only then is it
-// rounded to odd (truncated, the last bit set when anything was cut off),
-// which the rounding that follows cannot tell from the exact value.  So every
-// output is the formula's value rounded once, up to about 2^-43 relative, at
-// the price of two more instructions an element than a plain fp32 product.
+// a power of two, which costs the other rows nothing measurable); the squares
+// are summed with their rounding errors (two-sum) and then in fp64; s is held
+// as two fp32 numbers.  y in fp32 is on the same side of every value halfway
+// between two outputs as the exact y, unless it lies on such a value itself,
+// which its low bits show; only then is it rounded to odd (truncated, the last
+// bit set when anything was cut off), which the rounding that follows cannot
+// tell from the exact value.  So every output is the formula's value rounded
+// once, up to about 2^-43 relative, at the price of two more instructions an
+// element than a plain fp32 product.
 //
 // 8192 x 4096 fp16 with residual to MXFP8: 45 us, 5.3 TB/s (82 % of a plain
 // copy's; 40 us without any of the arithmetic, 42 with plain sums of squares).
@@ -448,7 +449,7 @@ int run_norm(const NormProblem& p) {
     e = launch_norm<T, FMT, 2>(p, a, static_cast<int>(t));
   else
     e = launch_norm<T, FMT, 1>(p, a, static_cast<int>(t));
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return launched(e);
 }
 
 template <class T, int FMT>
@@ -467,7 +468,7 @@ int run_convert(const ConvertProblem& p, bool to_mx) {
             : cudaLaunchKernelEx(&l.cfg, dequantize_kernel<T, FMT>,
                                  static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s),
                                  x, p.rows, p.cols, p.ldq, p.ldx, static_cast<int>(tiles));
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return launched(e);
 }
 
 template <class T>
