@@ -347,7 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   // no CTA of the pair leaves (or frees TMEM) while the other may still signal
   // its barriers or use its TMEM
-  cluster_sync();
+  __syncwarp();
+  cluster_arrive_relaxed();
+  cluster_wait();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after_sync();

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
+    cluster_arrive();
   } else if (warp == 1) {
     // ------------------------------------------- MMA issuer (pair leaders) ---
     if (leader) {
@@ -199,13 +200,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
+    __syncwarp();
+    cluster_arrive();
   } else {
     // -------------------------------- accumulator to shared memory (every CTA) ---
     int ok = 1;
     if (lane == 0) ok = mbar_wait(acc_full, 0, abort_flag, a.timeout_ns) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
+    // all loads of the pair have landed and all its MMAs have read them: the
+    // ring is free, for what others send, too
+    cluster_arrive();
     if (ok) {
-      // all loads of the pair have landed and all its MMAs have read them: the ring is free
       tc_fence_after_sync();
       const int q = warp & 3, g = (warp - 2) >> 2;
       float* mine = reinterpret_cast<float*>(smem) + q * 32 + lane;
@@ -225,7 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before_sync();
   fence_proxy_async_smem();  // the part is read by bulk copies
-  cluster_sync();            // all parts are written, all rings free
+  __syncthreads();           // all of this CTA's part is written
+  cluster_wait();            // all rings are free
   uint8_t* incoming = smem + C::kPartBytes;
   if (parts > 1) {
     if (threadIdx.x == 0) {
@@ -247,6 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (r1 > r0 && !mbar_wait(received, 0, nullptr, a.timeout_ns))
       raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 2);
   }
+  __syncwarp();
+  cluster_arrive_relaxed();  // what was sent to this CTA has left the others' shared memory
   if (*abort_flag == 0) {
     // items: 8 columns of C of one of this CTA's rows
     for (int it = threadIdx.x; it < (r1 - r0) * (kHalfN / 8); it += kThreads) {
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
-  cluster_sync();  // no CTA leaves while its copies may still read its shared memory
+  cluster_wait();  // no CTA leaves while its copies may still read its shared memory
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, C::kTmemCols);

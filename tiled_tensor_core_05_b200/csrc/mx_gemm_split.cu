@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kThreads)
   auto first_row = [&](int r) { return rows * r / splits; };
   const int r0 = first_row(rank), r1 = first_row(rank + 1);
   const int slot_bytes = (BN + splits - 1) / splits * kTileN * 4;
+  const bool pull = rows <= kPullRows;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kThreads)
         if (armed & (1u << s)) (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
       __syncwarp();
     }
+    if (splits > 1) cluster_arrive();
   } else if (warp == 1) {
     const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
     // rows 64 .. 127 of a scale tile are its columns 2 and 3
@@ -229,12 +231,15 @@ __global__ void __launch_bounds__(kThreads)
       }
       __syncwarp();
     }
+    if (splits > 1) cluster_arrive();
   } else {
     int ok = 1;
     if (lane == 0) ok = mbar_wait(acc_full, 0, abort_flag, a.timeout_ns) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
+    // all loads have landed and all MMAs have read them: the ring is free, for
+    // what others send, too
+    if (splits > 1 && !pull) cluster_arrive();
     if (ok) {
-      // all loads have landed and all MMAs have read them: the ring is free
       tc_fence_after_sync();
       const int q = warp & 3;
       float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
@@ -251,14 +256,16 @@ __global__ void __launch_bounds__(kThreads)
     } else if (lane == 0) {
       raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 1);
     }
+    __syncwarp();
+    if (splits > 1 && pull) cluster_arrive();  // the part is there to be read
   }
   __syncwarp();
   tc_fence_before_sync();
   uint8_t* incoming = smem + Cfg::kPartBytes;
-  const bool pull = rows <= kPullRows;
   if (splits > 1) {
     fence_proxy_async_smem();  // the part is read by bulk copies
-    cluster_sync();            // all parts are written, all rings free
+    __syncthreads();           // all of this CTA's part is written
+    cluster_wait();            // pull: all parts are; push: all rings are free
     if (!pull && threadIdx.x == 0) {
       mbar_arrive_expect_tx(received,
                             static_cast<uint32_t>((splits - 1) * (r1 - r0) * kTileN * 4));
@@ -281,38 +288,55 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
   }
 
-  if (*abort_flag == 0 && splits > 1 && pull) {
-    // items: 8 columns of a row, dealt out over the threads of the cluster
-    for (int it = rank * kThreads + threadIdx.x; it < rows * (kTileN / 8); it += splits * kThreads) {
-      const int m = it >> 4, c = (it & 15) * 8;
-      if (n0 + c >= a.out.N) continue;
-      float v[8] = {};
-      for (int s = 0; s < splits; ++s) {
+  const bool aborted = *abort_flag != 0;
+  if (splits > 1 && pull) {
+    // items: 8 columns of a row, at most one for a thread of the cluster
+    static_assert(kPullRows * (kTileN / 8) <= kThreads, "an item a thread");
+    const int m = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
+    const bool mine = rank == 0 && m < rows && n0 + c < a.out.N;
+    float v[8] = {};
+    if (mine) {
+      float4 p[8][2];  // all parts are on their way before the first is added
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        if (s >= splits) break;
         const uint32_t src = map_to_cta(
             smem_u32(smem) + static_cast<uint32_t>(m * kTileN + c) * 4, static_cast<uint32_t>(s));
-        add8(v, ld_cluster_f4(src), ld_cluster_f4(src + 16));
+        p[s][0] = ld_cluster_f4(src);
+        p[s][1] = ld_cluster_f4(src + 16);
       }
-      store_row8(a.out, m0 + m, n0 + c, v);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        if (s >= splits) break;
+        add8(v, p[s][0], p[s][1]);
+      }
     }
-  } else if (*abort_flag == 0) {
-    // items: 8 columns of one of this CTA's rows
-    for (int it = threadIdx.x; it < (r1 - r0) * (kTileN / 8); it += kThreads) {
-      const int m = it >> 4, c = (it & 15) * 8;
-      if (n0 + c >= a.out.N) continue;
-      float v[8] = {};
-      for (int s = 0; s < splits; ++s) {
-        const uint8_t* base = s == rank ? smem + r0 * kTileN * 4
-                                        : incoming + (s < rank ? s : s - 1) * slot_bytes;
-        const float4* src = reinterpret_cast<const float4*>(base) + (m * kTileN + c) / 4;
-        add8(v, src[0], src[1]);
+    __syncwarp();
+    cluster_arrive_relaxed();  // the others' parts have been read
+    if (mine && !aborted) store_row8(a.out, m0 + m, n0 + c, v);
+  } else {
+    __syncwarp();
+    if (splits > 1) cluster_arrive_relaxed();  // what was sent here has left the others' memory
+    if (!aborted) {
+      // items: 8 columns of one of this CTA's rows
+      for (int it = threadIdx.x; it < (r1 - r0) * (kTileN / 8); it += kThreads) {
+        const int m = it >> 4, c = (it & 15) * 8;
+        if (n0 + c >= a.out.N) continue;
+        float v[8] = {};
+        for (int s = 0; s < splits; ++s) {
+          const uint8_t* base = s == rank ? smem + r0 * kTileN * 4
+                                          : incoming + (s < rank ? s : s - 1) * slot_bytes;
+          const float4* src = reinterpret_cast<const float4*>(base) + (m * kTileN + c) / 4;
+          add8(v, src[0], src[1]);
+        }
+        store_row8(a.out, m0 + r0 + m, n0 + c, v);
       }
-      store_row8(a.out, m0 + r0 + m, n0 + c, v);
     }
   }
   __syncwarp();
   // no CTA leaves while another, or its own copies, may still read its shared memory
   if (splits > 1)
-    cluster_sync();
+    cluster_wait();
   else
     __syncthreads();
   if (warp == 1) {

@@ -163,6 +163,20 @@ __device__ __forceinline__ float2 finish2(float2 v, float2 b, int act) {
                            : v;
 }
 
+// cluster_sync in two halves: every thread arrives once, then waits once.  The
+// relaxed arrival is for threads that only say they are done with the shared
+// memory of others: a release waits for their stores to global memory (some
+// 1500 cycles at the end of a kernel).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
