@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dependency_trigger();
   grid_dependency_wait();
+  const int c = static_cast<int>(threadIdx.x & 15) * 8;  // the columns this thread finishes
+  const uint4 bias = load_bias(a.out, n0 + c);
 
   if (warp == 0) {
     // --------------------------------------------- TMA producer (every CTA) ---
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-    cluster_arrive();
+    cluster_arrive_relaxed();
   } else if (warp == 1) {
     // ------------------------------------------- MMA issuer (pair leaders) ---
     if (leader) {
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    cluster_arrive();
+    cluster_arrive_relaxed();
   } else {
     // -------------------------------- accumulator to shared memory (every CTA) ---
     int ok = 1;
@@ -209,19 +211,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = __shfl_sync(0xffffffffu, ok, 0);
     // all loads of the pair have landed and all its MMAs have read them: the
     // ring is free, for what others send, too
-    cluster_arrive();
+    cluster_arrive_relaxed();
     if (ok) {
       tc_fence_after_sync();
       const int q = warp & 3, g = (warp - 2) >> 2;
       float* mine = reinterpret_cast<float*>(smem) + q * 32 + lane;
 #pragma unroll 1
-      for (int c = g * 64; c < g * 64 + 64; c += 32) {
-        if (c >= rows) break;
+      for (int r = g * 64; r < g * 64 + 64; r += 32) {
+        if (r >= rows) break;
         uint32_t v[32];
-        tmem_load_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+        tmem_load_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + r, v);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (c + i < rows) mine[(c + i) * kHalfN] = __uint_as_float(v[i]);
+          if (r + i < rows) mine[(r + i) * kHalfN] = __uint_as_float(v[i]);
       }
     } else if (lane == 0) {
       raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 4);
@@ -255,21 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   cluster_arrive_relaxed();  // what was sent to this CTA has left the others' shared memory
-  if (*abort_flag == 0) {
-    // items: 8 columns of C of one of this CTA's rows
-    for (int it = threadIdx.x; it < (r1 - r0) * (kHalfN / 8); it += kThreads) {
-      const int m = it >> 4, c = (it & 15) * 8;
-      if (n0 + c >= a.out.N) continue;
-      float v[8] = {};
-      for (int s = 0; s < parts; ++s) {
-        const uint8_t* base = s == part ? smem + r0 * kHalfN * 4
-                                        : incoming + (s < part ? s : s - 1) * slot_bytes;
-        const float4* src = reinterpret_cast<const float4*>(base) + (m * kHalfN + c) / 4;
-        add8(v, src[0], src[1]);
-      }
-      store_row8(a.out, m0 + r0 + m, n0 + c, v);
-    }
-  }
+  if (*abort_flag == 0)
+    finish_rows<kThreads>(a.out, m0 + r0, n0 + c, r1 - r0, bias, parts, [&](int s) {
+      return reinterpret_cast<const float*>(
+                 s == part ? smem + r0 * kHalfN * 4
+                           : incoming + (s < part ? s : s - 1) * slot_bytes) + c;
+    });
   __syncwarp();
   cluster_wait();  // no CTA leaves while its copies may still read its shared memory
   if (warp == 1) {

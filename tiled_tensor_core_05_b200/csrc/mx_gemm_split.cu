@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t tmem = *tmem_slot;
   grid_dependency_trigger();
   grid_dependency_wait();
+  const int c = static_cast<int>(threadIdx.x & 15) * 8;  // the columns this thread finishes
+  const uint4 bias = load_bias(a.out, n0 + c);
 
   if (warp == 0) {
     int stage = 0;
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kThreads)
         if (armed & (1u << s)) (void)mbar_wait(&full[s], (parity >> s) & 1u, nullptr, a.timeout_ns);
       __syncwarp();
     }
-    if (splits > 1) cluster_arrive();
+    if (splits > 1) cluster_arrive_relaxed();
   } else if (warp == 1) {
     const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
     // rows 64 .. 127 of a scale tile are its columns 2 and 3
@@ -231,27 +233,27 @@ __global__ void __launch_bounds__(kThreads)
       }
       __syncwarp();
     }
-    if (splits > 1) cluster_arrive();
+    if (splits > 1) cluster_arrive_relaxed();
   } else {
     int ok = 1;
     if (lane == 0) ok = mbar_wait(acc_full, 0, abort_flag, a.timeout_ns) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     // all loads have landed and all MMAs have read them: the ring is free, for
     // what others send, too
-    if (splits > 1 && !pull) cluster_arrive();
+    if (splits > 1 && !pull) cluster_arrive_relaxed();
     if (ok) {
       tc_fence_after_sync();
       const int q = warp & 3;
       float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
       const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        if (c >= rows) break;
+      for (int r = 0; r < BN; r += 32) {
+        if (r >= rows) break;
         uint32_t v[32];
-        tmem_load_32x32b_x32(t_row + c, v);
+        tmem_load_32x32b_x32(t_row + r, v);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (c + i < rows) part[(c + i) * kTileN] = __uint_as_float(v[i]);
+          if (r + i < rows) part[(r + i) * kTileN] = __uint_as_float(v[i]);
       }
     } else if (lane == 0) {
       raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleEpilogue << 4) | 1);
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kThreads)
   if (splits > 1 && pull) {
     // items: 8 columns of a row, at most one for a thread of the cluster
     static_assert(kPullRows * (kTileN / 8) <= kThreads, "an item a thread");
-    const int m = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
+    const int m = threadIdx.x >> 4;
     const bool mine = rank == 0 && m < rows && n0 + c < a.out.N;
     float v[8] = {};
     if (mine) {
@@ -313,25 +315,19 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
     cluster_arrive_relaxed();  // the others' parts have been read
-    if (mine && !aborted) store_row8(a.out, m0 + m, n0 + c, v);
+    if (mine && !aborted)
+      with_columns(a.out, n0 + c, bias, [&](const auto& columns, auto act) {
+        columns.template store<decltype(act)::value>(m0 + m, v);
+      });
   } else {
     __syncwarp();
     if (splits > 1) cluster_arrive_relaxed();  // what was sent here has left the others' memory
-    if (!aborted) {
-      // items: 8 columns of one of this CTA's rows
-      for (int it = threadIdx.x; it < (r1 - r0) * (kTileN / 8); it += kThreads) {
-        const int m = it >> 4, c = (it & 15) * 8;
-        if (n0 + c >= a.out.N) continue;
-        float v[8] = {};
-        for (int s = 0; s < splits; ++s) {
-          const uint8_t* base = s == rank ? smem + r0 * kTileN * 4
-                                          : incoming + (s < rank ? s : s - 1) * slot_bytes;
-          const float4* src = reinterpret_cast<const float4*>(base) + (m * kTileN + c) / 4;
-          add8(v, src[0], src[1]);
-        }
-        store_row8(a.out, m0 + r0 + m, n0 + c, v);
-      }
-    }
+    if (!aborted)
+      finish_rows<kThreads>(a.out, m0 + r0, n0 + c, r1 - r0, bias, splits, [&](int s) {
+        return reinterpret_cast<const float*>(
+                   s == rank ? smem + r0 * kTileN * 4
+                             : incoming + (s < rank ? s : s - 1) * slot_bytes) + c;
+      });
   }
   __syncwarp();
   // no CTA leaves while another, or its own copies, may still read its shared memory

@@ -202,29 +202,77 @@ inline Output output_of(const MxGemmProblem& p) {
                 static_cast<int>(p.M),       static_cast<int>(p.N),             p.dtype, p.act};
 }
 
-// Eight columns of a row of C from their fp32 sums: bias, activation, one
-// rounding, stored as 16 bytes or, across the edge, one by one.
+// The 8 columns from n on of some rows of C, n the same for all rows a thread
+// finishes: what does not depend on the row is done once.
 template <class T>
-__device__ __forceinline__ void store_row8(const Output& o, int m, int n, const float (&v)[8]) {
-  const int count = min(8, o.N - n);
-  uint4 bias = make_uint4(0, 0, 0, 0);
-  if (o.bias != nullptr) bias = load8(o.bias + n, count);
-  float b[8], y[8];
-  unpack8<T>(bias, b);
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 r = finish2(make_float2(v[i], v[i + 1]), make_float2(b[i], b[i + 1]), o.act);
-    y[i] = r.x;
-    y[i + 1] = r.y;
+struct Columns {
+  uint16_t* C;
+  int64_t ldc;
+  int count;
+  float b[8];
+  __device__ __forceinline__ Columns(const Output& o, int n, const uint4& bias)
+      : C(o.C + n), ldc(o.ldc), count(min(8, o.N - n)) {
+    unpack8<T>(bias, b);
   }
-  store8(o.C + static_cast<int64_t>(m) * o.ldc + n, pack8<T>(y), count);
+  // a row from its fp32 sums: bias, activation, one rounding, stored as 16
+  // bytes or, across the edge, one by one
+  template <int ACT>
+  __device__ __forceinline__ void store(int m, const float (&v)[8]) const {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 r = activate2<ACT>(
+          __fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(b[i], b[i + 1])));
+      y[i] = r.x;
+      y[i + 1] = r.y;
+    }
+    store8(C + static_cast<int64_t>(m) * ldc, pack8<T>(y), count);
+  }
+};
+
+// The bias of the columns from n on (0 without one), for Columns: loaded while
+// the product's operands are still on their way.
+__device__ __forceinline__ uint4 load_bias(const Output& o, int n) {
+  if (o.bias == nullptr || n >= o.N) return make_uint4(0, 0, 0, 0);
+  return load8(o.bias + n, min(8, o.N - n));
 }
 
-__device__ __forceinline__ void store_row8(const Output& o, int m, int n, const float (&v)[8]) {
+// f(columns, activation) with the type and the activation as constants: a row
+// of the loop below is some 100 instructions, twice as many with them looked up
+// each time, and the last rows of a tile have nothing to hide them behind.
+template <class F>
+__device__ __forceinline__ void with_columns(const Output& o, int n, const uint4& bias, F&& f) {
+  auto typed = [&](auto columns) {
+    if (o.act == kActRelu)
+      f(columns, std::integral_constant<int, kActRelu>{});
+    else if (o.act == kActGelu)
+      f(columns, std::integral_constant<int, kActGelu>{});
+    else
+      f(columns, std::integral_constant<int, kActNone>{});
+  };
+  if (n >= o.N) return;
   if (o.dtype == MX_F16)
-    store_row8<__half>(o, m, n, v);
+    typed(Columns<__half>(o, n, bias));
   else
-    store_row8<__nv_bfloat16>(o, m, n, v);
+    typed(Columns<__nv_bfloat16>(o, n, bias));
+}
+
+// Rows m of C (m counts from m0) as the sums of their parts, in the order of
+// the parts; part(s) has the columns of this thread, 128 floats a row.  16
+// threads a row.
+template <int kThreads, class Part>
+__device__ __forceinline__ void finish_rows(const Output& o, int m0, int n, int rows,
+                                            const uint4& bias, int parts, Part&& part) {
+  with_columns(o, n, bias, [&](const auto& columns, auto act) {
+    for (int m = threadIdx.x >> 4; m < rows; m += kThreads / 16) {
+      float v[8] = {};
+      for (int s = 0; s < parts; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(part(s) + m * 128);
+        add8(v, src[0], src[1]);
+      }
+      columns.template store<decltype(act)::value>(m0 + m, v);
+    }
+  });
 }
 
 }  // namespace mx
