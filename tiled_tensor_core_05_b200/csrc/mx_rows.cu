@@ -11,15 +11,19 @@ namespace mx {
 namespace {
 
 // ------------------------------------------------------------------- quantise ---
-// One CTA per 128 x 128 tile of X: 16 threads read a row's 256 bytes, 16 rows
-// at a time, all 8 loads of a thread in flight before the first is used.  A
+// One CTA per 128 x 128 tile of X: 16 threads read a row's 256 bytes, 32 rows
+// at a time, all 4 loads of a thread in flight before the first is used.  A
 // block's maximum is shared by 4 lanes; the tile's 512 scale bytes are
 // collected in shared memory and written as one run.  8192 x 14336 fp16 to
 // MXFP8: 59 us, 6.0 TB/s (94 % of a plain copy's); to MXFP4 55 us, 5.4 TB/s.
-constexpr int kTileThreads = 256;
+// 256 threads with 8 loads each are slower by 3 % on 14336 x 4096 and 10 % on
+// 32 x 8192, 1024 threads by 15 % on large matrices.
+constexpr int kQuantThreads = 512;
+constexpr int kQuantRows = kQuantThreads / 16;      // rows at a time
+constexpr int kQuantLoads = kTileRows / kQuantRows;  // of a thread
 
 template <class T, int FMT>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kQuantThreads)
     quantize_kernel(const uint16_t* __restrict__ X, uint8_t* __restrict__ Q,
                     uint8_t* __restrict__ S, int64_t rows, int64_t cols, int64_t ldx, int64_t ldq,
                     int tiles) {
@@ -36,23 +40,23 @@ __global__ void __launch_bounds__(kTileThreads)
   grid_dependency_trigger();
   __syncthreads();
   grid_dependency_wait();
-  uint4 v[8];
+  uint4 v[kQuantLoads];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t r = row0 + 16 * j;
+  for (int j = 0; j < kQuantLoads; ++j) {
+    const int64_t r = row0 + kQuantRows * j;
     v[j] = make_uint4(0, 0, 0, 0);
     if (r < rows && n > 0) v[j] = load8(X + r * ldx + 8 * i, n);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t r = row0 + 16 * j;
+  for (int j = 0; j < kQuantLoads; ++j) {
+    const int64_t r = row0 + kQuantRows * j;
     float y[8];
     uint32_t e[2];
     unpack8<T>(v[j], y);
     const uint32_t byte = quantize8<FMT>(y, e);
     if (r < rows && n > 0) {
       store_elements<FMT>(Q + r * ldq, i, e, n);
-      const int rr = (t >> 4) + 16 * j;
+      const int rr = (t >> 4) + kQuantRows * j;
       if ((q & 3) == 0) scales[(rr & 31) * 16 + (rr >> 5) * 4 + (q >> 2)] = static_cast<uint8_t>(byte);
     }
   }
@@ -63,10 +67,12 @@ __global__ void __launch_bounds__(kTileThreads)
 }
 
 // ----------------------------------------------------------------- dequantise ---
-// The same tile and thread layout.  8192 x 14336 MXFP8: 55 us, 6.4 TB/s; MXFP4 47
-// us, 6.3 TB/s.
+// The same tile, 16 rows at a time: with 512 threads, 4 elements of 8 bytes in
+// flight each are too few (14336 x 4096 MXFP4 4 % slower).  8192 x 14336 MXFP8:
+// 55 us, 6.4 TB/s; MXFP4 47 us, 6.3 TB/s.
+constexpr int kDequantThreads = 256;
 template <class T, int FMT>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kDequantThreads)
     dequantize_kernel(const uint8_t* __restrict__ Q, const uint8_t* __restrict__ S,
                       uint16_t* __restrict__ X, int64_t rows, int64_t cols, int64_t ldq,
                       int64_t ldx, int tiles) {
@@ -457,7 +463,8 @@ int run_convert(const ConvertProblem& p, bool to_mx) {
   const int64_t tiles = scale_tiles(p.cols);
   const int64_t grid = tiles * ((p.rows + kTileRows - 1) / kTileRows);
   if (grid > INT32_MAX) return GEMM_ERR_INVALID_ARG;
-  Launch l(dim3(static_cast<unsigned>(grid)), dim3(kTileThreads), 0, p.stream);
+  Launch l(dim3(static_cast<unsigned>(grid)), dim3(to_mx ? kQuantThreads : kDequantThreads), 0,
+           p.stream);
   uint16_t* x = static_cast<uint16_t*>(const_cast<void*>(p.X));
   uint8_t* q = static_cast<uint8_t*>(const_cast<void*>(p.Q));
   uint8_t* s = static_cast<uint8_t*>(const_cast<void*>(p.S));
