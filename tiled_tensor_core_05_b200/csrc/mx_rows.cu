@@ -274,6 +274,9 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
   const uint16_t* r = a.R != nullptr ? a.R + row * a.ldr : nullptr;
   uint16_t* h = a.H != nullptr ? a.H + row * a.ldh : nullptr;
   uint4 hv[V > 0 ? V : 1];
+  // few rows: the weights are on their way beside h, not after the sum
+  constexpr bool kEarly = V == 1 || V == 2;
+  uint4 early[kEarly ? V : 1];
   float2 acc = make_float2(0.0f, 0.0f), err = make_float2(0.0f, 0.0f);
   // h is taken times c, a power of two: 1, unless the row's squares leave fp32's
   // range, which bf16 values can
@@ -297,6 +300,10 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
   if constexpr (V > 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v) hv[v] = load(x, threadIdx.x + v * tpr);
+    if constexpr (kEarly) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) early[v] = load(a.W, threadIdx.x + v * tpr);
+    }
     if (r != nullptr) {
       uint4 rv[V];
 #pragma unroll
@@ -370,8 +377,7 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
   const float sh = static_cast<float>(s);
   const float sl = static_cast<float>(s - static_cast<double>(sh));
 
-  auto emit = [&](int i, const uint4& u) {
-    const uint4 wv = load(a.W, i);
+  auto emit = [&](int i, const uint4& u, const uint4& wv) {
     const uint32_t* hw = reinterpret_cast<const uint32_t*>(&u);
     const uint32_t* ww = reinterpret_cast<const uint32_t*>(&wv);
     float f[8];
@@ -414,11 +420,17 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
   };
   if constexpr (V > 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) emit(threadIdx.x + v * tpr, hv[v]);
+    for (int v = 0; v < V; ++v) {
+      const int i = threadIdx.x + v * tpr;
+      if constexpr (kEarly)
+        emit(i, hv[v], early[v]);
+      else
+        emit(i, hv[v], load(a.W, i));
+    }
   } else {
     for (int v = 0; v < steps; ++v) {
       const int i = threadIdx.x + v * tpr;
-      emit(i, again(i));
+      emit(i, again(i), load(a.W, i));
     }
   }
 }
