@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kDequantThreads)
 // Precision: an MX element is decided by rounding at half steps, where the
 // last bits of y matter.  h^2 and h w are exact in fp32 (products of two
 // 16-bit values; a row of bf16 whose squares leave fp32's range is taken times
-// a power of two, which costs the other rows nothing measurable); the squares
+// a power of two, in a function of its own: 48.4 us a call as below in bf16,
+// 49.4 with that row's registers in this one); the squares
 // are summed with their rounding errors (two-sum) and then in fp64; s is held
 // as two fp32 numbers.  y in fp32 is on the same side of every value halfway
 // between two outputs as the exact y, unless it lies on such a value itself,
@@ -243,8 +244,13 @@ constexpr uint32_t kTieMask = FMT == MX_FP8   ? 0x7FFFFu
 template <int V>
 constexpr int kNormThreads = V >= 4 ? 512 : 1024;
 
-template <class T, int FMT, int V>
-__global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArgs a) {
+template <class T, int FMT>
+__device__ __noinline__ void norm_row_scaled(const NormArgs& a, float c);
+
+// The row of this thread; with kScaled, its h, which has been stored, is taken
+// times c.
+template <class T, int FMT, int V, bool kScaled>
+__device__ __forceinline__ void norm_row(const NormArgs& a, float c) {
   __shared__ double part[32];
   const int tpr = blockDim.x;
   const int lane = threadIdx.x & 31;
@@ -267,8 +273,10 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
     else if (i == whole && tail != 0)
       store8(p + 8 * static_cast<int64_t>(i), v, tail);
   };
-  grid_dependency_trigger();
-  grid_dependency_wait();
+  if (!kScaled) {
+    grid_dependency_trigger();
+    grid_dependency_wait();
+  }
 
   const uint16_t* x = a.X + row * a.ldx;
   const uint16_t* r = a.R != nullptr ? a.R + row * a.ldr : nullptr;
@@ -278,24 +286,29 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
   constexpr bool kEarly = V == 1 || V == 2;
   uint4 early[kEarly ? V : 1];
   float2 acc = make_float2(0.0f, 0.0f), err = make_float2(0.0f, 0.0f);
-  // h is taken times c, a power of two: 1, unless the row's squares leave fp32's
-  // range, which bf16 values can
-  constexpr bool kWide = std::is_same<T, __nv_bfloat16>::value;
-  float c = 1.0f;
-  auto values = [&](uint32_t w) {
-    const float2 v = unpack2<T>(w);
-    return kWide && c != 1.0f ? __fmul2_rn(v, splat2(c)) : v;
-  };
   auto squares = [&](const uint4& v) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) add_square(acc, err, values(w[k]));
+    for (int k = 0; k < 4; ++k) add_square(acc, err, unpack2<T>(w[k]));
   };
   // vector i of h once it has been stored, when there is no register copy
   auto again = [&](int i) {
-    if (r != nullptr && h != nullptr) return load(h, i);  // written by this thread
-    const uint4 u = load(x, i);
-    return r != nullptr ? add8<T>(u, load(r, i)) : u;
+    uint4 u;
+    if (r != nullptr && h != nullptr) {
+      u = load(h, i);  // written by this thread
+    } else {
+      u = load(x, i);
+      if (r != nullptr) u = add8<T>(u, load(r, i));
+    }
+    if constexpr (kScaled) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __fmul2_rn(unpack2<T>(w[k]), splat2(c));
+        w[k] = pack2<T>(f.x, f.y);
+      }
+    }
+    return u;
   };
   if constexpr (V > 0) {
 #pragma unroll
@@ -316,6 +329,8 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) squares(hv[v]);
+  } else if constexpr (kScaled) {
+    for (int v = 0; v < steps; ++v) squares(again(threadIdx.x + v * tpr));
   } else {
     for (int v = 0; v < steps; ++v) {
       const int i = threadIdx.x + v * tpr;
@@ -327,7 +342,7 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
       squares(u);
     }
   }
-  if constexpr (FMT != MX_NONE) {
+  if constexpr (FMT != MX_NONE && !kScaled) {
     // the rows that the last scale tile has no row for are cleared: 16 bytes of
     // a tile are rows l, l + 32, l + 64 and l + 96, dealt out over the threads
     // of the rows that it has (word by word, one row to MXFP8 takes 7.8 instead
@@ -353,8 +368,8 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
     }
   }
   const int wpr = tpr >> 5;
-  // mean of the squares + eps, of h c
-  auto mean = [&]() {
+  // mean of the squares + eps
+  auto mean = [&](double eps) {
     // an infinite sum has no rounding error (inf - inf is not one)
     double sum = (isinf(acc.x) || isinf(acc.y))
                      ? static_cast<double>(acc.x) + static_cast<double>(acc.y)
@@ -375,21 +390,17 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
     }
-    return fma(sum, a.inv_cols, static_cast<double>(a.eps) * c * c);
+    return fma(sum, a.inv_cols, eps);
   };
-  double m = mean();
-  if (kWide && !(m > 0x1p-80 && m < 0x1p127)) {  // the same for all threads of the row
-    // 2^80 takes bf16's smallest value to 2^-53, 2^-80 its largest to 2^48
-    c = m < 1.0 ? 0x1p80f : 0x1p-80f;
-    acc = err = make_float2(0.0f, 0.0f);
-    if (wpr > 1) __syncthreads();  // the parts have been read
-    if constexpr (V > 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) squares(hv[v]);
-    } else {
-      for (int v = 0; v < steps; ++v) squares(again(threadIdx.x + v * tpr));
+  const double m = mean(static_cast<double>(a.eps) * c * c);
+  // A row of bf16 whose squares leave fp32's range is read once more and taken
+  // times a power of two: 2^80 takes the smallest value to 2^-53, 2^-80 the
+  // largest to 2^48.  The same for all threads of the row.
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && !kScaled) {
+    if (!(m > 0x1p-80 && m < 0x1p127)) {
+      norm_row_scaled<T, FMT>(a, m < 1.0 ? 0x1p80f : 0x1p-80f);
+      return;
     }
-    m = mean();
   }
   const double s = inverse_sqrt(m);
   const float sh = static_cast<float>(s);
@@ -403,7 +414,7 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
     uint32_t low = ~0u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      p[k] = __fmul2_rn(values(hw[k]), unpack2<T>(ww[k]));
+      p[k] = __fmul2_rn(unpack2<T>(hw[k]), unpack2<T>(ww[k]));
       const float2 y = __ffma2_rn(p[k], splat2(sh), __fmul2_rn(p[k], splat2(sl)));
       low = min(low, min(__float_as_uint(y.x) & kTieMask<T, FMT>,
                          __float_as_uint(y.y) & kTieMask<T, FMT>));
@@ -451,6 +462,17 @@ __global__ void __launch_bounds__(kNormThreads<V>) rms_norm_kernel(const NormArg
       emit(i, again(i), load(a.W, i));
     }
   }
+}
+
+template <class T, int FMT>
+__device__ __noinline__ void norm_row_scaled(const NormArgs& a, float c) {
+  norm_row<T, FMT, 0, true>(a, c);
+}
+
+template <class T, int FMT, int V>
+__global__ void __launch_bounds__(kNormThreads<V>)
+    rms_norm_kernel(const __grid_constant__ NormArgs a) {
+  norm_row<T, FMT, V, false>(a, 1.0f);
 }
 
 template <class T, int FMT, int V>
