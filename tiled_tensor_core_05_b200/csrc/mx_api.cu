@@ -97,13 +97,13 @@ int run_gemm(const MxGemmProblem& p) {
   if (rc == GEMM_OK) rc = check_mx(p.B, p.SB, p.N, p.K, p.ldb, p.format, d.device);
   if (rc != GEMM_OK) return rc;
   // Measured (us: split kernel, pair kernel, pair tiles with K divided):
-  //   1500 x 2000 x 2000 MXFP4 (48 tiles of 256 x 256)   17.9   8.7  16.9
-  //   1024 x 4096 x 8192 MXFP8 (64)                      49.0  27.8  42.0
-  //   256 x 9000 x 4096 MXFP8 (36)                       17.0  17.1  15.3
-  //   256 x 4096 x 8192 MXFP8 (16)                       17.4  24.5  15.7
-  //   512 x 2048 x 2048 MXFP4 (16; 8 k-blocks)            7.9   7.6   8.2
-  //   128 x 18944 x 4096 MXFP4 (74, half empty)          13.7  14.0  14.1
-  //   100 x 28672 x 8192 MXFP4 (112; two waves split)    34.2  29.2  32.1
+  //   1500 x 2000 x 2000 MXFP4 (48 tiles of 256 x 256)   15.9   8.2  14.0
+  //   1024 x 4096 x 8192 MXFP8 (64)                      46.8  27.2  38.9
+  //   256 x 9000 x 4096 MXFP8 (36)                       16.0  16.8  13.8
+  //   256 x 4096 x 8192 MXFP8 (16)                       19.7  24.2  14.3
+  //   512 x 2048 x 2048 MXFP4 (16; 8 k-blocks)            6.1   7.3   6.8
+  //   128 x 18944 x 4096 MXFP4 (74, half empty)          13.1  13.7  12.8
+  //   100 x 28672 x 8192 MXFP4 (112; two waves split)    32.6  28.9  29.6
   // So: the pair kernel where its tiles fill half the SMs, if they are not half
   // empty (M > 128) or the split kernel's would take two waves;
   // else K divided among pairs from 65 rows and 16 k-blocks on; else the split

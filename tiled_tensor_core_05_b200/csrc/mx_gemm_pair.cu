@@ -22,12 +22,16 @@
 //     instructions and two special-function results an element, nearly as long
 //     as the MMAs of a 4-bit tile with K = 4096.
 //
-// Measured: 8192^3 MXFP8 + ReLU 369 us (2.98 PFLOP/s, the tensor pipe active for
-// 90 % of the cycles; 444 us back to back under the power cap), 8192 x 14336 x
-// 4096 MXFP4 + bias + GELU 190 us (5.07 PFLOP/s), without an epilogue to speak
-// of and K = 16384 590 us (6.52 PFLOP/s).  A 4-bit k-block takes 346 ns, of which
-// the 4 MMAs 270 and the 6 scale copies the rest; a tile costs 1.5 us besides
-// (handing over the shared columns 0.6, the stores 0.9), 2.2 with GELU.
+// Measured: 8192^3 MXFP8 + ReLU 361 us (3.05 PFLOP/s; 431 us back to back under
+// the power cap), 8192 x 14336 x 4096 MXFP4 + bias + GELU 188 us (5.11 PFLOP/s),
+// without an epilogue to speak of and K = 16384 590 us (6.52 PFLOP/s).  Bound by
+// the tensor pipe at the clock that the power limit leaves (1.31 to 1.45 GHz in
+// these launches): a tile of 64 k-blocks takes 34,000 cycles, its MMAs alone some
+// 32,800, the hand-over of the shared columns the rest; of 16 k-blocks (K = 4096 in
+// 4 bits) 9,700 for 8,200, and 10,500 with GELU, whose instructions slow the MMA
+// warp's.  Asking for the next stage's barrier before this one's MMAs, and copying
+// a tile's first scales before the columns are free, takes 200 cycles off a tile
+// and nothing off the time.
 #include "mx_internal.h"
 #include "mx_umma.cuh"
 #include "tile_common.cuh"

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kDequantThreads)
 // once, up to about 2^-43 relative, at the price of two more instructions an
 // element than a plain fp32 product.
 //
-// 8192 x 4096 fp16 with residual to MXFP8: 45 us, 5.3 TB/s (82 % of a plain
+// 8192 x 4096 fp16 with residual to MXFP8: 45 us, 5.2 TB/s (81 % of a plain
 // copy's; 40 us without any of the arithmetic, 42 with plain sums of squares).
 // Rows prefetched by a persistent grid: 57 us, the registers cost more
 // occupancy than the prefetch brings; 8 vectors a thread 66 us.
