@@ -562,6 +562,27 @@ def test_same_bits_on_every_run():
         assert torch.equal(ttc.gemm_mx(a, b), c)
 
 
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+def test_few_rows_back_to_back(M, fmt):
+    """Up to 4 rows with K divided read the parts from the other CTAs' shared memory: launch
+    after launch, products of two shapes in turn, each with the sums of its own operands (exact
+    in fp32, so equal bits)."""
+    rng = np.random.default_rng(100 + M)
+    cases = []
+    for N, K in ((300, 2000), (1000, 4100), (130, 8200)):
+        a, b = exact_operand(rng, M, K, fmt), exact_operand(rng, N, K, fmt)
+        want = ref.round_to(ref.values(*a, fmt) @ ref.values(*b, fmt).T, torch.float16)
+        out = torch.empty((40, M, (N + 7) // 8 * 8), dtype=torch.float16, device="cuda")
+        cases.append((make_mx(*a, fmt), make_mx(*b, fmt), want, out, N))
+    for i in range(40):
+        for a, b, _, out, N in cases:
+            ttc.gemm_mx(a, b, out=out[i, :, :N])
+    for _, _, want, out, N in cases:
+        for i in range(40):
+            assert np.array_equal(ref.to_np(out[i, :, :N]), want), (N, i)
+
+
 # -------------------------------------------------------------------------- refusals ---
 
 

@@ -315,7 +315,10 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncwarp();
-    cluster_arrive_relaxed();  // the others' parts have been read
+    // The others' parts have been read: a release, since the loads above have to
+    // be over before their owners leave.  (Nothing has been stored to global
+    // memory yet that it would wait for.)
+    cluster_arrive();
     if (mine && !aborted)
       with_columns(a.out, n0 + c, bias, [&](const auto& columns, auto act) {
         columns.template store<decltype(act)::value>(m0 + m, v);

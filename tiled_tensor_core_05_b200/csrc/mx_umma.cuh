@@ -164,9 +164,10 @@ __device__ __forceinline__ float2 finish2(float2 v, float2 b, int act) {
 }
 
 // cluster_sync in two halves: every thread arrives once, then waits once.  The
-// relaxed arrival is for threads that only say they are done with the shared
-// memory of others: a release waits for their stores to global memory (some
-// 1500 cycles at the end of a kernel).
+// relaxed arrival orders nothing before it: it is for threads whose use of the
+// others' shared memory has been seen to end (an mbarrier they waited for).
+// A release waits for the thread's stores to global memory, too (some 1500
+// cycles at the end of a kernel).
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
