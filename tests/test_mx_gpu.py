@@ -583,6 +583,30 @@ def test_few_rows_back_to_back(M, fmt):
             assert np.array_equal(ref.to_np(out[i, :, :N]), want), (N, i)
 
 
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+def test_pair_tiles_back_to_back(fmt):
+    """The CTA-pair kernel launch after launch, shapes in turn with 1 to 5 tiles a pair (each
+    buffer of the accumulator last, and not handed back), the last rows and columns nearly empty
+    (warps with nothing to store)."""
+    rng = np.random.default_rng(77)
+    K = 96
+    cases = []
+    for M, N in ((257, 9300), (1537, 2700), (2305, 4400), (3841, 4900), (4609, 4700)):
+        a, b = exact_operand(rng, M, K, fmt), exact_operand(rng, N, K, fmt)
+        want = torch.as_tensor(ref.round_to(ref.values(*a, fmt) @ ref.values(*b, fmt).T,
+                                            torch.float16)).half().cuda()
+        out = torch.empty((M, (N + 7) // 8 * 8), dtype=torch.float16, device="cuda")[:, :N]
+        cases.append((make_mx(*a, fmt), make_mx(*b, fmt), want, out,
+                      torch.ones((), dtype=torch.bool, device="cuda")))
+    for _ in range(10):
+        for a, b, want, out, same in cases:
+            ttc.gemm_mx(a, b, out=out)
+        for a, b, want, out, same in cases:
+            same &= (out == want).all()
+            out.fill_(7.0)
+    assert all(bool(c[4]) for c in cases)
+
+
 # -------------------------------------------------------------------------- refusals ---
 
 

@@ -339,8 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the columns both buffers share: the last ones of buffer 0, the first of buffer 1
         const bool shares = buf == 0 ? (g + 1) * kWarpCols > Cfg::kAcc1
                                      : g * kWarpCols < Cfg::kOverlap;
-        if (shares) mbar_arrive_cluster_relaxed(shared_empty_leader);
-        mbar_arrive_cluster_relaxed(acc_empty_leader + buf * 8);
+        // Only where a later tile's MMAs wait for it: nothing else would keep
+        // the leader from ending before an arrival of the other CTA lands.
+        if (shares && tile + npairs < num_tiles) mbar_arrive_cluster_relaxed(shared_empty_leader);
+        if (tile + 2 * npairs < num_tiles) mbar_arrive_cluster_relaxed(acc_empty_leader + buf * 8);
       }
       store_columns<T, ACT>(v, a, row0 + lane, col0, policy);
       buf ^= 1;
@@ -349,8 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before_sync();
-  // no CTA of the pair leaves (or frees TMEM) while the other may still signal
-  // its barriers or use its TMEM
+  // No CTA of the pair frees TMEM while the other may still use it.  (A relaxed
+  // arrival: every signal that the epilogues send to the leader's barriers has
+  // been waited for by its MMA warp.)
   __syncwarp();
   cluster_arrive_relaxed();
   cluster_wait();
