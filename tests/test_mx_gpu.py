@@ -607,6 +607,27 @@ def test_pair_tiles_back_to_back(fmt):
     assert all(bool(c[4]) for c in cases)
 
 
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+def test_pairs_whose_ring_does_not_fill(fmt):
+    """Both CTA-pair kernels with fewer k-blocks than ring stages, as many and some more, launch
+    after launch: producers leave only after every stage they filled has been released."""
+    rng = np.random.default_rng(78)
+    step = 128 if fmt == "mxfp8" else 256  # elements of a k-block
+    cases = []
+    for M, N, blocks in [(300, 9500, n) for n in (1, 5, 6, 7, 12, 13)] + \
+                        [(70, 300, n) for n in (16, 31, 32, 33, 35)]:
+        K = blocks * step - 7
+        a, b = exact_operand(rng, M, K, fmt), exact_operand(rng, N, K, fmt)
+        want = ref.round_to(ref.values(*a, fmt) @ ref.values(*b, fmt).T, torch.float16)
+        cases.append((make_mx(*a, fmt), make_mx(*b, fmt), torch.as_tensor(want).half().cuda()))
+    got = []
+    for _ in range(5):
+        got.append([ttc.gemm_mx(a, b) for a, b, _ in cases])
+    for outs in got:
+        for c, (_, _, want) in zip(outs, cases):
+            assert torch.equal(c, want)
+
+
 # -------------------------------------------------------------------------- refusals ---
 
 

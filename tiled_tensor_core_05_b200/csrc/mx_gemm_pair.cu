@@ -223,6 +223,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // The stages' last uses are over, too: the leader's commits arrive here, and
+    // this CTA must not end before the last of them has.
+    for (int s = 0; s < kStages && ok; ++s) {
+      ok = mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
     if (!ok) {
       if (lane == 0)
         raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleProducer << 4) | 3);
@@ -353,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   // No CTA of the pair frees TMEM while the other may still use it.  (A relaxed
   // arrival: every signal that the epilogues send to the leader's barriers has
-  // been waited for by its MMA warp.)
+  // been waited for by its MMA warp, and every commit of its to the other CTA's
+  // by that CTA's producer and epilogue.)
   __syncwarp();
   cluster_arrive_relaxed();
   cluster_wait();

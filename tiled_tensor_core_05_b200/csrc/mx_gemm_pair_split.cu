@@ -149,6 +149,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1u;
       }
     }
+    // The stages' last uses are over, too: the leader's commits arrive here, and
+    // this CTA must not end before the last of them has.
+    for (int s = 0; s < kStages && ok; ++s) {
+      ok = mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag, a.timeout_ns);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
     if (!ok) {
       if (lane == 0)
         raise_abort(a.status, abort_flag, kStatusTimeoutBase | (kRoleProducer << 4) | 4);
@@ -267,7 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                            : incoming + (s < part ? s : s - 1) * slot_bytes) + c;
     });
   __syncwarp();
-  cluster_wait();  // no CTA leaves while its copies may still read its shared memory
+  // no CTA leaves while its copies may still read its shared memory (the
+  // leader's commits have been waited for by producers and epilogues)
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, C::kTmemCols);
