@@ -683,6 +683,50 @@ def test_refusals_of_pointers_and_strides():
     torch.cuda.synchronize()
 
 
+def test_refusals_of_extents_past_64_bits():
+    """Rows and strides whose product passes 2^64 and comes back as a few bytes; everything else
+    about the calls is in order (scales and single rows lie in a buffer that holds them)."""
+    n, ld16, ld8 = (1 << 25) + 1, 1 << 38, 1 << 39  # n rows of 2^39 bytes: 2^64 and a row
+    buf = torch.zeros(1 << 29, dtype=torch.uint8, device="cuda")
+    S, row, P = (buf.data_ptr() + (k << 27) for k in (0, 2, 3))
+    assert ttc.mx_scale_bytes(n, 32) <= 2 << 27 and 2 * n <= 1 << 27
+    Q, W, R, small = (P + k * 65536 for k in (1, 2, 3, 4))
+    for fmt in (1, 2):
+        assert raw("mx_quantize", P, Q, S, n, 32, ld16, ld8, 0, fmt) == -1
+        assert raw("mx_dequantize", Q, S, P, n, 32, ld8, ld16, 0, fmt) == -1
+        assert raw("mx_rms_norm", P, None, W, None, Q, S, n, 32, ld16, 0, 0, ld8, 1e-6, 0, fmt) == -1
+        assert raw("mx_gemm", P, S, Q, small, None, R, n, 8, 32, ld8, 32, ld16, fmt, 0, 0) == -1
+        assert raw("mx_gemm", P, small, Q, S, None, row, 1, n, 32, 32, ld8, n + 7, fmt, 0, 0) == -1
+        assert raw("mx_gemm", P, S, Q, small, None, R, n, 8, 0, ld8, 32, ld16, fmt, 0, 0) == -1
+    assert raw("mx_rms_norm", P, None, W, None, Q, None, n, 32, ld16, 0, 0, ld16, 1e-6, 0, 0) == -1
+    assert raw("mx_rms_norm", P, R, W, R, Q, None, n, 32, ld16, ld16, ld16, ld16, 1e-6, 0, 0) == -1
+    torch.cuda.synchronize()
+    assert not buf.any()
+
+
+def test_refusals_of_fp16_extents_past_64_bits():
+    """The same of the fp16 products and the activation, which share the checks."""
+    from tiled_tensor_core_05_b200 import ops
+    lib, n, ld = ops.lib(), (1 << 25) + 1, 1 << 38
+    buf = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    row, P = buf.data_ptr(), buf.data_ptr() + (1 << 27)
+    Q, C = P + 65536, P + 131072
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def general(A, B, out, M, N, K, lda, ldb, ldc, ta=0, tb=0):
+        return lib.gemm_f16_general(A, B, None, out, M, N, K, lda, ldb, ldc, ta, tb, 0, 0, stream)
+
+    assert general(P, Q, C, n, 32, 32, ld, 32, ld) == -1
+    assert general(P, Q, C, n, 32, 0, 32, 32, ld) == -1       # nothing but the output
+    assert general(row, Q, C, 1, 32, n, n + 7, ld, 32) == -1
+    assert general(P, Q, C, 32, 32, n, ld, ld, 32, ta=1) == -1
+    assert general(P, Q, row, 1, n, 32, 32, ld, n + 7, tb=1) == -1
+    assert lib.gemm_activation_f32(P, C, 1 << 62, 1, stream) == -1
+    assert lib.gemm_activation_f32(P, C, (1 << 62) + 8, 2, stream) == -1
+    torch.cuda.synchronize()
+    assert not buf.any()
+
+
 def test_refusals_of_the_python_layer():
     t = torch.float16
     x = torch.zeros(8, 64, dtype=t, device="cuda")

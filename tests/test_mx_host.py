@@ -138,6 +138,39 @@ def test_python_refusals(ttc):
             ttc.MxTensor(*bad)
 
 
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_extents_past_64_bits(tmp_path):
+    """The size of an operand and whether an allocation holds it, for the sizes and strides that
+    the entry points admit: rows below 2^31, rows less than 2^40 bytes apart."""
+    src = tmp_path / "extent.cc"
+    src.write_text('#include <stdio.h>\n#include "extent.h"\nint main() {\n'
+                   "  long long r, u, l, t; unsigned long long p, b, n;\n"
+                   '  while (scanf("%lld %lld %lld %lld %llu %llu %llu", &r, &u, &l, &t, &p, &b, &n) '
+                   "== 7) {\n    const uint64_t s = ttc::matrix_span(r, u, l, t);\n"
+                   '    printf("%llu %d\\n", (unsigned long long)s, ttc::span_inside(p, s, b, n));\n'
+                   "  }\n}\n")
+    exe = tmp_path / "extent"
+    csrc = os.path.join(ROOT, "tiled_tensor_core_05_b200", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Wextra", "-Werror", "-I", csrc, str(src), "-o",
+                    str(exe)], check=True)
+    base, size = 1 << 40, 1 << 21
+    operands = [(1, 64, 64, 2), (8, 64, 64, 1), (2 ** 25 + 1, 64, 2 ** 38, 2),
+                (2 ** 24 + 1, 64, 2 ** 39, 2), (2 ** 25 + 1, 64, 2 ** 39, 1),
+                (2 ** 31 - 1, 8, 2 ** 40 - 16, 1), (2 ** 31 - 1, 8, 2 ** 39 - 8, 2),
+                (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 + 7, 2), (1, 2 ** 62, 2 ** 62, 4),
+                (1, 2 ** 62 + 3, 2 ** 62 + 3, 4), (2 ** 24, 16, 2 ** 39, 2), (2 ** 24 + 1, 0, 2 ** 39, 2),
+                (1, size // 2, size // 2, 2), (1, size // 2 + 1, size, 2)]
+    rows = [(*o, base + at, base, size) for o in operands
+            for at in (0, 16, size - 128, size - 16, size, size + 16, -16, 2 ** 63, 2 ** 64 - 2 ** 41)]
+    rows = [(*r[:4], r[4] % 2 ** 64, *r[5:]) for r in rows]
+    out = subprocess.run([str(exe)], input="\n".join(" ".join(map(str, r)) for r in rows),
+                         capture_output=True, text=True, check=True).stdout.split("\n")
+    for (n, used, ld, unit, p, b, s), line in zip(rows, out):
+        span = ((n - 1) * ld + used) * unit
+        want = min(span, 2 ** 64 - 1)
+        assert line == f"{want} {int(b <= p and p + span <= b + s)}", (n, used, ld, unit, p - b)
+
+
 # ------------------------------------------------- the plain implementation itself ---
 
 

@@ -31,8 +31,8 @@ COMMON = ["host_common.cu"]  # linked into both libraries
 SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu"]
 MX_SOURCES = ["mx_api.cu", "mx_rows.cu", "mx_gemm_split.cu", "mx_gemm_pair.cu",
               "mx_gemm_pair_split.cu"]
-HEADERS = ["sm100.cuh", "internal.h", "skinny_common.cuh", "tile_common.cuh", "mx_internal.h", "mx_common.cuh",
-           "mx_umma.cuh"]
+HEADERS = ["sm100.cuh", "extent.h", "internal.h", "skinny_common.cuh", "tile_common.cuh",
+           "mx_internal.h", "mx_common.cuh", "mx_umma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",

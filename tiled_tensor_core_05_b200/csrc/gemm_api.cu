@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/gemm_f16.h"
+#include "extent.h"
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -28,18 +29,12 @@ struct Workspace {
 };
 std::vector<Workspace> g_workspaces;
 
-// Bytes from the first to the last element of an fp16 matrix.
-uint64_t fp16_span(int64_t rows, int64_t cols, int64_t ld) {
-  return (static_cast<uint64_t>(rows - 1) * static_cast<uint64_t>(ld) +
-          static_cast<uint64_t>(cols)) * 2u;
-}
-
 int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int device) {
   if (p == nullptr) return GEMM_ERR_INVALID_ARG;
   if (ld < cols || ld < 1) return GEMM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0 || (ld & 7) != 0) return GEMM_ERR_ALIGNMENT;
   if (static_cast<uint64_t>(ld) * 2u >= (1ull << 40)) return GEMM_ERR_INVALID_ARG;
-  return check_device_range(p, device, fp16_span(rows, cols, ld));
+  return check_device_range(p, device, matrix_span(rows, cols, ld, 2));
 }
 
 int get_workspace(const DeviceCtx& d, cudaStream_t stream, void** ptr, size_t* bytes) {
@@ -489,7 +484,7 @@ int gemm_activation_f32(const void* x, void* y, int64_t n, int activation,
   int rc = get_device(&d);
   if (rc != GEMM_OK) return rc;
   load_entry_points();
-  const uint64_t span = 4u * static_cast<uint64_t>(n);
+  const uint64_t span = matrix_span(1, n, n, 4);
   if (query_pointer(x, d.device, span) != 1 || query_pointer(y, d.device, span) != 1)
     return GEMM_ERR_INVALID_ARG;
   int64_t blocks = (n + 255) / 256;

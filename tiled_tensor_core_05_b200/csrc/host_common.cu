@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/gemm_f16.h"
+#include "extent.h"
 #include "internal.h"
 
 namespace ttc {
@@ -61,8 +62,7 @@ bool extent_in_allocation(const void* p, uint64_t span) {
   CUdeviceptr base = 0;
   size_t size = 0;
   if (g_addr_range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return false;
-  const uint64_t start = reinterpret_cast<uint64_t>(p);
-  return start >= base && start - base + span <= size;
+  return span_inside(reinterpret_cast<uint64_t>(p), span, base, size);
 }
 
 }  // namespace
@@ -138,8 +138,7 @@ int query_pointer(const void* p, int device, uint64_t span) {
   if (g_ptr_attrs(5, attrs, data, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return 0;
   const bool on_device = (mem_type == CU_MEMORYTYPE_DEVICE && ordinal == device) || managed != 0;
   if (!on_device || size == 0) return 0;
-  const uint64_t start = reinterpret_cast<uint64_t>(p);
-  return (start >= base && start - base + span <= size) ? 1 : 0;
+  return span_inside(reinterpret_cast<uint64_t>(p), span, base, size) ? 1 : 0;
 }
 
 int check_device_range(const void* p, int device, uint64_t span) {

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "extent.h"
 #include "mx_common.cuh"
 #include "mx_internal.h"
 
@@ -26,9 +27,7 @@ int check_bytes(const void* p, uint64_t span, int device) {
 int check_rows(const void* p, int64_t rows, int64_t used, int64_t ld, int unit, int device) {
   if (p == nullptr || ld < used || ld >= (1ll << 40) / unit) return GEMM_ERR_INVALID_ARG;
   if ((ld * unit & 15) != 0) return GEMM_ERR_ALIGNMENT;
-  const uint64_t span = (static_cast<uint64_t>(rows - 1) * static_cast<uint64_t>(ld) +
-                         static_cast<uint64_t>(used)) * static_cast<uint64_t>(unit);
-  return check_bytes(p, span, device);
+  return check_bytes(p, matrix_span(rows, used, ld, unit), device);
 }
 
 int check_mx(const void* data, const void* scales, int64_t rows, int64_t cols, int64_t ld,
