@@ -46,8 +46,10 @@ FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustain
 # committed ncu capture is reported only while these are unchanged)
 KERNEL_SOURCES = {
     "tile_pair_gemm_kernel": ["tiled_tensor_core_05_b200/csrc/gemm_tile.cu",
+                              "tiled_tensor_core_05_b200/csrc/tile_common.cuh",
                               "tiled_tensor_core_05_b200/csrc/sm100.cuh"],
     "tile_gemm_kernel": ["tiled_tensor_core_05_b200/csrc/gemm_tile.cu",
+                         "tiled_tensor_core_05_b200/csrc/tile_common.cuh",
                          "tiled_tensor_core_05_b200/csrc/sm100.cuh"],
     "skinny_gemm_kernel": ["tiled_tensor_core_05_b200/csrc/gemm_skinny.cu",
                            "tiled_tensor_core_05_b200/csrc/skinny_common.cuh",

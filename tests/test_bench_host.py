@@ -4,6 +4,7 @@ JSON line of the reference arm (the CPU oracle) on a small workload."""
 import io
 import json
 import os
+import re
 import sys
 import time
 from contextlib import redirect_stdout
@@ -61,6 +62,31 @@ def test_traffic_is_reported_only_for_the_captured_source(lib, tmp_path, monkeyp
     monkeypatch.setattr(bench, "kernel_source_hash", lambda k: "0" * 16)
     assert bench.traffic_for("cube8192", "tile_pair_gemm_kernel") is None
     assert bench.traffic_for("cube256", "tile_gemm_kernel") is None  # never captured
+
+
+@pytest.mark.parametrize("kernel", sorted(bench.KERNEL_SOURCES))
+def test_kernel_sources_are_whole(kernel):
+    """Every file of device code that a kernel's source includes counts as its source."""
+    csrc = os.path.join(ROOT, "tiled_tensor_core_05_b200", "csrc")
+    todo, seen = [bench.KERNEL_SOURCES[kernel][0]], set()
+    while todo:
+        rel = todo.pop()
+        if rel in seen:
+            continue
+        seen.add(rel)
+        with open(os.path.join(ROOT, rel)) as f:
+            for name in re.findall(r'#include "([^"/]+\.cuh)"', f.read()):
+                todo.append(os.path.relpath(os.path.join(csrc, name), ROOT))
+    assert seen == set(bench.KERNEL_SOURCES[kernel])
+
+
+def test_traffic_table_is_of_the_current_sources():
+    """The committed captures are of the kernels as they are: no figure of the bench is missing."""
+    with open(os.path.join(ROOT, "profiles", "traffic.json")) as f:
+        table = json.load(f)
+    for key, rec in table.items():
+        kernel, workload, *variant = key.split("/")
+        assert bench.traffic_for(workload, kernel, *variant) == rec["dram_bytes_per_launch"], key
 
 
 def test_traffic_is_keyed_by_variant(tmp_path, monkeypatch):

@@ -1,6 +1,8 @@
-// Helpers shared by the persistent tile kernels (gemm_tile.cu and
-// mx_gemm_pair.cu): tile order, the epilogue's bias loads and staged stores of
-// 16-bit elements, launch set-up.
+// Helpers of the tile kernels: tile order, the abort path's wait and launch
+// set-up, which gemm_tile.cu shares with the CTA-pair kernels of the
+// microscaled products (mx_gemm_pair.cu, mx_gemm_pair_split.cu), and the
+// epilogue's bias loads and staged stores of fp16 elements, which only
+// gemm_tile.cu uses.
 #pragma once
 
 #include <atomic>
