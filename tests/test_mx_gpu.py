@@ -727,6 +727,34 @@ def test_refusals_of_fp16_extents_past_64_bits():
     assert not buf.any()
 
 
+@pytest.mark.parametrize("library", ["mx", "fp16"])
+def test_failed_status_query_is_not_reported_again(library):
+    """The status of a stream that is being captured cannot be read; the error is that call's, not
+    the next one's, whose kernel runs."""
+    import ctypes
+    from tiled_tensor_core_05_b200 import ops
+    rt = ctypes.CDLL("libcudart.so.12")  # torch's, as it is loaded
+    stream = torch.cuda.Stream()
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    x = torch.randn(8, 64, device="cuda").half()
+    want = ttc.mx_quantize(x, "mxfp8") if library == "mx" else ops.gemm_f16(x, x.t().contiguous())
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(handle, 2) == 0  # relaxed mode
+    with pytest.raises(RuntimeError):
+        (ttc.mx_device_status if library == "mx" else ops.device_status)(stream=stream)
+    graph = ctypes.c_void_p()
+    rt.cudaStreamEndCapture(handle, ctypes.byref(graph))  # (the query has ended the capture)
+    assert not graph.value
+    rt.cudaGetLastError()
+    if library == "mx":
+        got = ttc.mx_quantize(x, "mxfp8")
+        assert torch.equal(got.data, want.data) and torch.equal(got.scales, want.scales)
+        assert ttc.mx_device_status() == 0
+    else:
+        assert torch.equal(ops.gemm_f16(x, x.t().contiguous()), want)
+        assert ops.device_status() == 0
+
+
 def test_refusals_of_the_python_layer():
     t = torch.float16
     x = torch.zeros(8, 64, dtype=t, device="cuda")

@@ -136,16 +136,16 @@ int read_and_clear_status(const DeviceCtx& d, cudaStream_t stream, int* out) {
   if (cudaMemcpyAsync(&host, d.status, sizeof(int), cudaMemcpyDeviceToHost, stream) !=
           cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
-    return GEMM_ERR_LAUNCH;
+    return runtime_error();
   if (host != 0) {
     if (cudaMemsetAsync(d.status, 0, sizeof(int), stream) != cudaSuccess)
-      return GEMM_ERR_LAUNCH;
+      return runtime_error();
     // a kernel that gave up may have left split-K arrival counters non-zero
     std::lock_guard<std::mutex> lock(g_mutex);
     for (const Workspace& w : g_workspaces)
       if (w.device == d.device && cudaMemsetAsync(w.ptr, 0, w.bytes, stream) != cudaSuccess)
-        return GEMM_ERR_LAUNCH;
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return GEMM_ERR_LAUNCH;
+        return runtime_error();
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return runtime_error();
   }
   *out = host;
   return GEMM_OK;

@@ -91,7 +91,7 @@ void load_entry_points() {
 // ------------------------------------------------------------ device state ---
 int get_device(DeviceCtx* ctx) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_LAUNCH;
+  if (cudaGetDevice(&dev) != cudaSuccess) return runtime_error();
   if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED_DEVICE;
   std::lock_guard<std::mutex> lock(g_devices_mutex);
   DeviceEntry& e = g_devices[dev];
@@ -100,14 +100,14 @@ int get_device(DeviceCtx* ctx) {
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return GEMM_ERR_LAUNCH;
+      return runtime_error();
     e.supported = (major == 10 && minor == 0);
     e.sm_count = sms;
     if (e.supported) {
       // The symbol's device address for this device (host code cannot use the
       // symbol itself as a pointer).
       void* p = nullptr;
-      if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return GEMM_ERR_LAUNCH;
+      if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return runtime_error();
       e.status = static_cast<int*>(p);
     }
     e.ready = true;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/gemm_f16.h"
+
 namespace ttc {
 
 struct GemmProblem {
@@ -67,6 +69,13 @@ struct DeviceCtx {
 
 // The current device's context (host_common.cu).  Returns 0 or a GEMM_ERR_* code.
 int get_device(DeviceCtx* ctx);
+
+// The status of a CUDA runtime call that failed.  The runtime's last error is
+// cleared: this call reports it, not the next one that launches a kernel.
+inline int runtime_error() {
+  cudaGetLastError();
+  return GEMM_ERR_LAUNCH;
+}
 
 // Resolves the driver entry points the checks and tensor maps use (once).
 void load_entry_points();

@@ -179,10 +179,10 @@ int mx_get_device_status(gemm_stream_t stream, int* device_status) {
   if (cudaMemcpyAsync(&host, d.status, sizeof(int), cudaMemcpyDeviceToHost, stream) !=
           cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
-    return GEMM_ERR_LAUNCH;
+    return runtime_error();
   if (host != 0 && (cudaMemsetAsync(d.status, 0, sizeof(int), stream) != cudaSuccess ||
                     cudaStreamSynchronize(stream) != cudaSuccess))
-    return GEMM_ERR_LAUNCH;
+    return runtime_error();
   *device_status = host;
   return GEMM_OK;
 }

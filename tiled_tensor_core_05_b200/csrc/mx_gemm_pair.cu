@@ -381,7 +381,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
   static std::atomic<int> max_pairs[64] = {};  // resident pairs, per device (0 = not asked yet)
   auto kern = pair_gemm_kernel<FMT, T, ACT>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, d.device, attr_done))
-    return GEMM_ERR_LAUNCH;
+    return runtime_error();
   const int64_t row_bytes = mx_row_bytes(p.K, FMT);
   const int64_t sf_tiles = scale_tiles(p.K);
   constexpr int kBox = Kind<FMT>::kSfTiles;

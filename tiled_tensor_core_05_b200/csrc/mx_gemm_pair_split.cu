@@ -292,7 +292,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
   static Residency residency[64];
   auto kern = pair_split_gemm_kernel<FMT>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, d.device, attr_done))
-    return GEMM_ERR_LAUNCH;
+    return runtime_error();
   const int64_t row_bytes = mx_row_bytes(p.K, FMT);
   const int64_t sf_tiles = scale_tiles(p.K);
   const int64_t num_kb = (row_bytes + kRowBytes - 1) / kRowBytes;

@@ -412,7 +412,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d, int splits) {
 
 template <int FMT, int BN, bool DEEP>
 int launch_depth(const MxGemmProblem& p, const DeviceCtx& d, int64_t tiles) {
-  if (!set_attributes<FMT, BN, DEEP>(d)) return GEMM_ERR_LAUNCH;
+  if (!set_attributes<FMT, BN, DEEP>(d)) return runtime_error();
   const int64_t stages = (mx_row_bytes(p.K, FMT) + kRowBytes - 1) / kRowBytes;
   return launch<FMT, BN, DEEP>(p, d, choose_splits<FMT, BN, DEEP>(tiles, stages, d));
 }

@@ -66,12 +66,8 @@ struct Launch {
   }
 };
 
-// The status of a launch.  CUDA's last error is cleared either way: it is
-// reported here, not by a later call of another library.
-inline int launched(cudaError_t e) {
-  const cudaError_t last = cudaGetLastError();
-  return e == cudaSuccess && last == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
-}
+// The status of a launch, by what the launch itself returned.
+inline int launched(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : runtime_error(); }
 
 // How many clusters of c CTAs (c = 2 .. 8) of a kernel the GPU holds at one CTA
 // an SM, asked once per device: the GPCs leave SMs over.
