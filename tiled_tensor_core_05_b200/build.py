@@ -85,10 +85,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with cf.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
         bind = ex.submit(_build_bind, verbose)
         objs = dict(zip(sources, ex.map(lambda s: _compile(s, ptxas_info, verbose), sources)))
-    bind.result()
     # only the extern "C" API is exported: gemm_* of libttc05, mx_* of libttcmx
     _link(MX_LIB, [objs[s] for s in COMMON + MX_SOURCES], "mx_*", verbose)
     _link(LIB, [objs[s] for s in COMMON + SOURCES], "gemm_*", verbose)
+    bind.result()  # needs g++ and torch's headers, which the libraries do not
     return LIB
 
 
