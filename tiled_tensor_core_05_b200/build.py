@@ -25,7 +25,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libttc05.so")
 MX_LIB = os.path.join(PKG, "libttcmx.so")
-BIND = os.path.join(PKG, "_mxbind.so")  # CPython binding of libttcmx, against the torch in use
 BIND_SOURCE = "mx_bind.cpp"
 COMMON = ["host_common.cu"]  # linked into both libraries
 SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu"]
@@ -47,6 +46,17 @@ def nvcc() -> str:
     return cand
 
 
+def bind_path() -> str:
+    """The CPython binding of libttcmx for the interpreter and the torch in use: its name holds
+    what it is compiled against, so that another version builds, and loads, one of its own."""
+    import sysconfig
+
+    import torch
+    return os.path.join(PKG, f"_mxbind.torch{torch.__version__}"
+                        f".cxx11abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+                        + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def _inputs():
     files = [os.path.join(CSRC, s) for s in COMMON + SOURCES + MX_SOURCES + HEADERS + [BIND_SOURCE]]
     files += [os.path.join(INCLUDE, h) for h in ("gemm_f16.h", "gemm_mx.h")]
@@ -55,7 +65,10 @@ def _inputs():
 
 
 def needs_build() -> bool:
-    built = (LIB, MX_LIB, BIND)
+    try:
+        built = (LIB, MX_LIB, bind_path())
+    except ImportError:  # no torch: the binding has yet to be built
+        return True
     if not all(os.path.exists(f) for f in built):
         return True
     t = min(os.path.getmtime(f) for f in built)
@@ -99,7 +112,8 @@ def _build_bind(verbose: bool) -> None:
     import torch
     from torch.utils import cpp_extension
     lib_dir = cpp_extension.library_paths()[0]
-    tmp = BIND + f".tmp{os.getpid()}"
+    bind = bind_path()
+    tmp = bind + f".tmp{os.getpid()}"
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            "-fvisibility=hidden",
@@ -114,7 +128,7 @@ def _build_bind(verbose: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND)
+    os.replace(tmp, bind)
 
 
 def _link(lib: str, objs: list, exports: str, verbose: bool) -> None:

@@ -23,15 +23,13 @@ import os
 
 import torch
 
-from . import ops
+from . import build, ops
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libttcmx.so")
 
 FORMATS = {"mxfp8": 1, "mxfp4": 2}
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 BLOCK = 32
-
-BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mxbind.so")
 
 _lib = None
 _bind = None
@@ -53,7 +51,8 @@ def mx_lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib, _bind
     if _lib is None:
-        for path in (LIB_PATH, BIND_PATH):
+        bind_path = build.bind_path()
+        for path in (LIB_PATH, bind_path):
             if not os.path.exists(path):
                 raise RuntimeError(
                     f"{path} is missing: build it with "
@@ -63,7 +62,7 @@ def mx_lib() -> ctypes.CDLL:
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res
-        spec = importlib.util.spec_from_file_location("_mxbind", BIND_PATH)
+        spec = importlib.util.spec_from_file_location("_mxbind", bind_path)
         bind = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(bind)
         bind.bind(*(ctypes.cast(getattr(handle, name), _p).value for name in
