@@ -109,6 +109,8 @@ GEMM_API int mx_rms_norm(const void* X, const void* R, const void* W, void* H, v
  *   C: M x N of type `dtype`, row stride ldc in elements;
  *   activation: a gemm_activation value.
  * Products and sums are fp32; C is rounded once.  K == 0 gives C = act(bias).
+ * GELU is x Phi(x), before the rounding right to 2^-18 + x^2 2^-22 relative, down
+ * its negative tail, too (NaN for -infinity).
  * An output whose row of A or of B holds a NaN block is NaN (+0 after ReLU,
  * which maps NaN to +0). */
 GEMM_API int mx_gemm(const void* A, const void* SA, const void* B, const void* SB,

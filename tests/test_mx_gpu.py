@@ -1,6 +1,8 @@
 """The microscaled operators on the GPU against the plain 64-bit implementation
 of ``mx_ref``: quantisation and the norm's MX output bit by bit, products exactly
 where the sums are exact and within a derived bound otherwise."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -378,6 +380,46 @@ def test_scales_from_end_to_end(M):
     want = ref.round_to(ref.values(*a, "mxfp8") @ ref.values(*b, "mxfp8").T, torch.float16)
     got = ttc.gemm_mx(make_mx(*a, "mxfp8"), make_mx(*b, "mxfp8"))
     assert np.array_equal(ref.to_np(got), want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kernel", ["fill", "split", "pair", "pair_split"])
+def test_gelu_of_every_value(kernel, dtype):
+    """GELU down its negative tail, in each kernel: the bias runs over all values of the type and
+    the product adds 0, so what is rounded is GELU of the bias alone.
+
+    Bound on the value before it is rounded, relative: the square in the exponent has five
+    roundings of 2^-24 (the factor and its product, twice each, and the square itself), x^2 / 2
+    times that, below x^2 2^-22.6; the fit 2^-20.8; exp2, the reciprocal, the coefficients and some
+    ten operations 2^-24 to 2^-22 each, below 2^-19.  Beyond |x| = 40 GELU is x or 0 in fp32.
+    Subnormal fp32 results are off by 2^-149, and what is flushed to 0 is below 2^-135 (half of
+    bf16's smallest value is 2^-134).  The output's rounding adds half a step."""
+    t = DTYPES[dtype]
+    v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(t)
+    if kernel == "pair_split":  # fewer columns: the tail, the largest values, those that are none
+        v = torch.cat((v[(v < -(2.0 ** -4)) & (v > -15)], v[v > 1000][-20:], v[v < -1000][-20:],
+                       v[torch.isnan(v)][::50]))
+    M = {"fill": 3, "split": 2, "pair": 200, "pair_split": 70}[kernel]
+    K = {"fill": 0, "split": 40, "pair": 40, "pair_split": 2100}[kernel]
+    x = v.double().numpy()
+    bias = dev_vec(x, t)
+    if K:
+        a, b = (make_mx(np.zeros((n, K), np.uint8), np.full((n, -(-K // 32)), 127, np.uint8),
+                        "mxfp8") for n in (M, x.size))
+    else:
+        a, b = (ttc.mx_empty(n, 0, "mxfp8", "cuda") for n in (M, x.size))
+    got = ttc.gemm_mx(a, b, bias, "gelu", dtype=t)
+    assert torch.equal(got.view(torch.int16), got[:1].view(torch.int16).expand_as(got))
+    y = ref.to_np(got[0])
+    # (ref.act is right to 2^-53 of x, which is nothing in the tail; erfc is right there)
+    with np.errstate(invalid="ignore"):
+        want = 0.5 * x * torch.special.erfc(torch.from_numpy(-x * math.sqrt(0.5))).numpy()
+    kept = np.isfinite(x)
+    assert np.array_equal(y[~kept], want[~kept], equal_nan=True)  # inf, and NaN for -inf and NaN
+    x, y, want = x[kept], y[kept], want[kept]
+    off = np.abs(want) * (2.0 ** -18 + np.minimum(x * x, 1600) * 2.0 ** -22) + 2.0 ** -135
+    assert (np.abs(y - want) <= off * (1 + ref.HALF[t]) + ref.HALF[t] * np.abs(want)
+            + ref.TINY[t]).all()
 
 
 def test_product_without_elements():

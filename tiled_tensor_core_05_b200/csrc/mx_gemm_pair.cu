@@ -111,7 +111,7 @@ __device__ __forceinline__ void store_columns(const uint32_t (&v)[kWarpCols], co
     for (int k = 0; k < 8; ++k) {
       float2 x = make_float2(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
       if (a.bias != nullptr) x = __fadd2_rn(x, unpack2<T>(bw[k]));
-      x = activate2<ACT>(x);
+      x = mx_activate2<ACT>(x);
       h[k] = pack2<T>(x.x, x.y);
     }
     if (row >= a.M) continue;
