@@ -24,6 +24,7 @@ constexpr int kTileN = 256;   // rows of B per pair
 constexpr int kHalfN = 128;   // and per CTA
 constexpr int kTileM = 128;   // rows of A per pair
 constexpr int kHalfM = 64;    // of which a CTA stages
+constexpr int kMaxParts = 4;  // pairs of a cluster
 constexpr int kStages = 8;
 constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, 64 rows of A each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -42,7 +43,7 @@ struct Cfg {
   static constexpr int kSetCols = 2 * Kind<FMT>::kSfCols;
   static constexpr uint32_t kTmemCols = 256;
   static_assert(kTileM + kStages * kSetCols <= 256, "TMEM columns");
-  static_assert(2 * kPartBytes <= kRing, "parts");
+  static_assert(kPartBytes + slot_rows(kTileM, kMaxParts) * kHalfN * 4 <= kRing, "parts");
   static_assert(kSmemBytes <= kMaxDynamicSmem, "shared memory budget");
 };
 
@@ -300,7 +301,7 @@ int launch(const MxGemmProblem& p, const DeviceCtx& d) {
   const int64_t tiles = tiles_m * ((p.N + kTileN - 1) / kTileN);
   // as many parts of at least four k-blocks as run in one wave
   int parts = 1;
-  for (int s = 2; s <= 4 && num_kb >= 4 * s; ++s)
+  for (int s = 2; s <= kMaxParts && num_kb >= 4 * s; ++s)
     if (tiles <= residency[d.device & 63].of(2 * s, kern, kThreads, C::kSmemBytes, d)) parts = s;
   if (2 * parts * tiles > INT32_MAX) return GEMM_ERR_INVALID_ARG;
   constexpr int kBox = Kind<FMT>::kSfTiles;

@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kTileN = 128;  // columns of C per tile
+constexpr int kMaxSplits = 8;  // CTAs of a cluster
 constexpr int kPullRows = 4;  // up to so many rows the parts are read, not sent
 
 template <int FMT, int BN, bool DEEP>
@@ -51,7 +52,7 @@ struct SplitCfg {
   static constexpr int kPartBytes = BN * kTileN * 4;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kSmemBytes = 1024 + kRing + (2 * kStages + 3) * 8 + 16;
-  static_assert(2 * kPartBytes <= kRing, "parts");
+  static_assert(kPartBytes + slot_rows(BN, kMaxSplits) * kTileN * 4 <= kRing, "parts");
   // accumulator, then one set of scales per stage: a stage's columns are
   // written again only after the MMAs that read them have completed
   static constexpr int kSfBase = BN < 32 ? 32 : BN;
@@ -299,9 +300,9 @@ __global__ void __launch_bounds__(kThreads)
     const bool mine = rank == 0 && m < rows && n0 + c < a.out.N;
     float v[8] = {};
     if (mine) {
-      float4 p[8][2];  // all parts are on their way before the first is added
+      float4 p[kMaxSplits][2];  // all parts are on their way before the first is added
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < kMaxSplits; ++s) {
         if (s >= splits) break;
         const uint32_t src = map_to_cta(
             smem_u32(smem) + static_cast<uint32_t>(m * kTileN + c) * 4, static_cast<uint32_t>(s));
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreads)
         p[s][1] = ld_cluster_f4(src + 16);
       }
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < kMaxSplits; ++s) {
         if (s >= splits) break;
         add8(v, p[s][0], p[s][1]);
       }
@@ -353,7 +354,7 @@ int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   using Cfg = SplitCfg<FMT, BN, DEEP>;
   static Residency residency[64];
   int splits = 1;
-  for (int c = 2; c <= 8 && stages >= 4 * c; ++c) {
+  for (int c = 2; c <= kMaxSplits && stages >= 4 * c; ++c) {
     const int n = residency[d.device & 63].of(c, split_gemm_kernel<FMT, BN, DEEP>, kThreads,
                                               Cfg::kSmemBytes, d);
     if (tiles <= static_cast<int64_t>(n) * Cfg::kPerSm) splits = c;

@@ -241,6 +241,18 @@ __device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float
   v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
 }
 
+// Rows that a CTA has slots for in the kernels that divide K: of a tile of
+// `rows` rows in n parts it finishes up to ceil(rows / n) and is sent them by the
+// n - 1 others; the most over n <= max_parts (16 rows: 18 with 7 parts).
+constexpr int slot_rows(int rows, int max_parts) {
+  int most = 0;
+  for (int n = 2; n <= max_parts; ++n) {
+    const int r = (n - 1) * ((rows + n - 1) / n);
+    most = r > most ? r : most;
+  }
+  return most;
+}
+
 // What the epilogues of the kernels that divide K need of C.
 struct Output {
   uint16_t* C;
