@@ -431,6 +431,82 @@ def test_product_without_elements():
         assert not ttc.gemm_mx(a, b, dtype=t).any()
 
 
+# ------------------------------------------- every kernel that a size can take ---
+# (148 SMs; the norm has 4, 2 or 1 vectors a thread, or reads its rows twice; a product takes
+# the split kernel, with one CTA an SM and a deep ring or two, its K in 1 to 8 parts, the pair
+# split kernel in 1 to 4 parts, or the pair kernel)
+
+
+@pytest.mark.parametrize("rows,cols", [(4800, 300), (2400, 1100), (620, 8000), (310, 16000)],
+                         ids=["one_warp", "two_warps", "eight_warps", "sixteen_warps"])
+@pytest.mark.parametrize("fmt", [None, "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rms_norm_of_many_rows(rows, cols, fmt, dtype):
+    """Four vectors a thread: rows * threads a row from 1024 * 148 on."""
+    test_rms_norm(rows, cols, fmt, dtype, (rows + cols) % 20 == 0)
+
+
+@pytest.mark.parametrize("rows,cols", [(620, 4090), (300, 8100)])
+@pytest.mark.parametrize("fmt", [None, "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("residual", [True, False], ids=["res", "plain"])
+def test_rms_norm_of_some_rows(rows, cols, fmt, residual):
+    """Two vectors a thread, loaded together with the weights."""
+    test_rms_norm(rows, cols, fmt, "bf16", residual)
+
+
+@pytest.mark.parametrize("fmt", [None, "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("rows,cols", [(4810, 260), (950, 4100), (480, 10000)])
+def test_rms_norm_of_many_rows_where_squares_leave_fp32(rows, cols, fmt):
+    """bf16 rows of every size among each other, several of them in a CTA."""
+    t = torch.bfloat16
+    rng = np.random.default_rng(rows)
+    size = np.exp2(rng.choice([-131.0, -90, -80, -41, 0, 0, 0, 40, 63, 64, 125], rows))[:, None]
+    x = host16(np.clip(rng.standard_normal((rows, cols)), -3.9, 3.9) * size, t)
+    w = host16(1 + 0.1 * rng.standard_normal(cols), t)
+    want = ref.norm(x, w, 0.0)
+    got = ttc.rms_norm(dev16(x, t), dev_vec(w, t), 0.0, format=fmt)
+    if fmt is None:
+        assert np.array_equal(ref.to_np(got), ref.round_to(want, t))
+    else:
+        codes, scales = ref.quantize(want, fmt)
+        assert np.array_equal(got.scales.cpu().numpy(), ref.tile_scales(scales, cols))
+        data = got.data.cpu().numpy()[:, :ref.row_bytes(cols, fmt)]
+        assert np.array_equal(data, ref.pack(codes, fmt))
+
+
+# one CTA an SM, K whole, in rings of 10, 9 and 8 stages that fill and do not; then more tiles
+# than SMs; then the pair split kernel in 3, 2, 1 parts and with several rows of tiles
+OTHER_KERNELS = [(1, 9700, 600), (1, 9700, 4200), (4, 18900, 1300), (16, 14336, 3000),
+                 (20, 12000, 300), (32, 9601, 3000), (40, 10000, 300), (64, 12345, 2100),
+                 (128, 9473, 1000), (20, 20000, 300), (3, 28672, 700), (100, 20000, 500),
+                 (70, 5000, 4200), (70, 8000, 4200), (100, 12000, 4200), (200, 4000, 4200),
+                 (129, 6000, 4300), (256, 4096, 4200)]
+
+
+@pytest.mark.parametrize("M,N,K", OTHER_KERNELS)
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+def test_product_of_exact_sums_in_every_kernel(M, N, K, fmt):
+    test_product_of_exact_sums(M, N, K, fmt, "bf16" if (M + N) % 2 else "fp16")
+
+
+@pytest.mark.parametrize("parts", range(1, 9))
+@pytest.mark.parametrize("M", [2, 15, 30, 59])
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+def test_product_in_any_number_of_parts(parts, M, fmt):
+    """K in 1 to 8 parts of four k-blocks and a few more, read (2 rows) and sent, rows that the
+    parts do not divide evenly."""
+    K = (4 * parts + min(parts, 3)) * (128 if fmt == "mxfp8" else 256) - 40
+    test_product_of_exact_sums(M, 200, K, fmt, "fp16")
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 10000, 1500), (33, 9999, 1500), (70, 5000, 4200),
+                                   (90, 8000, 2100), (100, 10001, 4200)])
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+@pytest.mark.parametrize("act", ["relu", "gelu"])
+def test_product_with_bias_in_every_kernel(M, N, K, fmt, act):
+    test_product(M, N, K, fmt, "bf16" if K == 1500 else "fp16", act, True)
+
+
 # -------------------------------------------------------------- together, in use ---
 
 
