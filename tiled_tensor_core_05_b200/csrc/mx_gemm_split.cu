@@ -317,9 +317,13 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
     // The others' parts have been read: a release, since the loads above have to
-    // be over before their owners leave.  (Nothing has been stored to global
-    // memory yet that it would wait for.)
-    cluster_arrive();
+    // be over before their owners leave.  Only this CTA has read any.  (1 x 1024 x
+    // 1024 MXFP8: 3.97 us, 4.10 where all release, 3.84 without an order; 2 x 2048 x
+    // 8192: 6.66, 6.91 and 6.65.)
+    if (rank == 0)
+      cluster_arrive();
+    else
+      cluster_arrive_relaxed();
     if (mine && !aborted)
       with_columns(a.out, n0 + c, bias, [&](const auto& columns, auto act) {
         columns.template store<decltype(act)::value>(m0 + m, v);
