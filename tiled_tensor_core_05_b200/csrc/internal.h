@@ -1,4 +1,5 @@
-// Host-side declarations shared by the translation units of libttc05.
+// Host-side declarations shared by the translation units of libttc05 and, the
+// device context, checks and tensor maps among them, of libttcmx.
 #pragma once
 
 #include <cuda.h>

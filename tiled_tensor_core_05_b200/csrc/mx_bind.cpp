@@ -1,7 +1,8 @@
 // CPython binding of the microscaled operators: argument checks, allocation of
 // outputs and marshalling into the C ABI of include/gemm_mx.h, for the calls
 // whose kernels take no longer than such work takes in Python (a norm of one
-// token: 5 us on the GPU; 18 us of checks, torch.empty and ctypes before).
+// token: 2.9 us on the GPU, 7.5 us here and in mx.py on the host; 18 us with the
+// checks, torch.empty and ctypes in Python).
 // mx.py is the only caller; it hands over the addresses of the library's entry
 // points.  Errors of arguments raise here; status codes of the library are
 // returned, for mx.py to raise.

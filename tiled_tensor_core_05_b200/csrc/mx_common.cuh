@@ -17,7 +17,6 @@
 namespace ttc {
 namespace mx {
 
-constexpr int kBlock = 32;       // elements that share a scale
 constexpr int kTileRows = 128;   // rows of a scale tile
 constexpr int kTileCols = 128;   // columns of a scale tile (4 blocks)
 constexpr int kTileBytes = 512;

@@ -22,8 +22,8 @@
 //     instructions and two special-function results an element, nearly as long
 //     as the MMAs of a 4-bit tile with K = 4096.
 //
-// Measured: 8192^3 MXFP8 + ReLU 361 us (3.05 PFLOP/s; 431 us back to back under
-// the power cap), 8192 x 14336 x 4096 MXFP4 + bias + GELU 188 us (5.11 PFLOP/s),
+// Measured: 8192^3 MXFP8 + ReLU 362 us (3.04 PFLOP/s; 431 us back to back under
+// the power cap), 8192 x 14336 x 4096 MXFP4 + bias + GELU 187 us (5.15 PFLOP/s),
 // without an epilogue to speak of and K = 16384 590 us (6.52 PFLOP/s).  Bound by
 // the tensor pipe at the clock that the power limit leaves (1.31 to 1.45 GHz in
 // these launches): a tile of 64 k-blocks takes 34,000 cycles, its MMAs alone some
@@ -350,6 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : g * kWarpCols < Cfg::kOverlap;
         // Only where a later tile's MMAs wait for it: nothing else would keep
         // the leader from ending before an arrival of the other CTA lands.
+        // (1500 x 2000 x 2000 MXFP4 7.86 us; 8.29 with every arrival and a
+        // closing barrier that releases, 7.72 without either.)
         if (shares && tile + npairs < num_tiles) mbar_arrive_cluster_relaxed(shared_empty_leader);
         if (tile + 2 * npairs < num_tiles) mbar_arrive_cluster_relaxed(acc_empty_leader + buf * 8);
       }

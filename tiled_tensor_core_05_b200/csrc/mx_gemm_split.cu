@@ -8,16 +8,17 @@
 // every other CTA the rows that one owns (one bulk copy between the SMs'
 // shared memories each), and adds the parts of its own rows in rank order.
 // Nothing is kept in device memory between or during calls (no workspace, no
-// counters), and the order of the sums is fixed by the shape.  Reading the
-// other CTAs' parts with loads instead runs at some 8 bytes a clock and SM (60 x
-// 4096 x 8192 MXFP8: 15.0 us, 11.6 with copies, 10.9 now; 16 x 2048 x 8192: 7.6 and
-// 7.0);
-// it is done only for a few rows, where waiting for the copies costs more (1 x
-// 8192 x 4096 MXFP8: 8.6 us, 9.2 with copies, 8.4 now).
+// counters), and the order of the sums is fixed by the shape.  Up to 4 rows the
+// parts are read from the other CTAs' shared memory instead of sent: loads run
+// at some 8 bytes a clock and SM, too slow for more rows (60 x 4096 x 8192 MXFP8:
+// 15.0 us, 11.6 with copies when this was tried), but a few rows would wait
+// longer for the copies (1 x 8192 x 4096 MXFP8: 8.6 us, 9.2 with copies then;
+// 8.5 now).
 //
 // Bound by reading B from device memory where it is large (32 x 28672 x 8192
-// MXFP4: 22.0 us, 5.7 TB/s; 1 x 28672 x 4096 MXFP8: 20.5 us, 5.8 TB/s), else by a
-// chain of 3.4 us (1 x 1024 x 1024 MXFP4) to 6 us: launch, first load, accumulator, joining, store.
+// MXFP4: 22.8 us, 5.5 TB/s; 1 x 28672 x 4096 MXFP8: 21.6 us, 5.6 TB/s), else by a
+// chain of 4 us (1 x 1024 x 1024 MXFP8) to 6 us: launch, first load, accumulator,
+// joining, store.
 //
 //   warp 0   TMA producer: elements by tensor maps into 128-byte-swizzled
 //            shared memory, scale tiles by plain bulk copies

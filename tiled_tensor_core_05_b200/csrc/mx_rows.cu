@@ -162,6 +162,8 @@ __global__ void __launch_bounds__(kDequantThreads)
 // copy's; 40 us without any of the arithmetic, 42 with plain sums of squares).
 // Rows prefetched by a persistent grid: 57 us, the registers cost more
 // occupancy than the prefetch brings; 8 vectors a thread 66 us.
+// With V = 0 (beyond 16384 columns, h read twice) 2048 x 32768 to MXFP8 takes 139
+// us, 3.4 TB/s.
 constexpr int64_t kSms = 148;  // of a B200, to choose V
 
 struct NormArgs {
