@@ -1,5 +1,6 @@
-"""Build ``libttc05.so`` (the fp16 GEMM kernels and their C ABI) and
-``libttcmx.so`` (the microscaled operators) in-tree with nvcc.
+"""Build ``libttc05.so`` (the fp16 GEMM kernels and their C ABI), ``libttcmx.so``
+(the microscaled operators) and ``libttcff.so`` (the feed-forward operators)
+in-tree with nvcc.
 
     python -m tiled_tensor_core_05_b200.build [--force] [--verbose] [--ptxas-info]
 
@@ -25,13 +26,16 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libttc05.so")
 MX_LIB = os.path.join(PKG, "libttcmx.so")
-BIND_SOURCE = "mx_bind.cpp"
-COMMON = ["host_common.cu"]  # linked into both libraries
+FF_LIB = os.path.join(PKG, "libttcff.so")
+BIND_SOURCES = ["mx_bind.cpp", "ff_bind.cpp"]
+COMMON = ["host_common.cu"]  # linked into every library
 SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu"]
 MX_SOURCES = ["mx_api.cu", "mx_rows.cu", "mx_gemm_split.cu", "mx_gemm_pair.cu",
               "mx_gemm_pair_split.cu"]
+FF_SOURCES = ["ff_api.cu", "ff_pair.cu", "ff_split.cu", "ff_rows.cu", "ff_w4.cu"]
 HEADERS = ["sm100.cuh", "extent.h", "internal.h", "skinny_common.cuh", "tile_common.cuh",
-           "mx_internal.h", "mx_common.cuh", "mx_umma.cuh"]
+           "mx_internal.h", "mx_common.cuh", "mx_umma.cuh", "ff_internal.h", "ff_common.cuh",
+           "bind_common.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -47,7 +51,7 @@ def nvcc() -> str:
 
 
 def bind_path() -> str:
-    """The CPython binding of libttcmx for the interpreter and the torch in use: its name holds
+    """The CPython bindings of libttcmx and libttcff, in one file, for the interpreter and the torch in use: its name holds
     what it is compiled against, so that another version builds, and loads, one of its own."""
     import sysconfig
 
@@ -58,15 +62,16 @@ def bind_path() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in COMMON + SOURCES + MX_SOURCES + HEADERS + [BIND_SOURCE]]
-    files += [os.path.join(INCLUDE, h) for h in ("gemm_f16.h", "gemm_mx.h")]
+    files = [os.path.join(CSRC, s)
+             for s in COMMON + SOURCES + MX_SOURCES + FF_SOURCES + HEADERS + BIND_SOURCES]
+    files += [os.path.join(INCLUDE, h) for h in ("gemm_f16.h", "gemm_mx.h", "gemm_ff.h")]
     files.append(os.path.abspath(__file__))
     return files
 
 
 def needs_build() -> bool:
     try:
-        built = (LIB, MX_LIB, bind_path())
+        built = (LIB, MX_LIB, FF_LIB, bind_path())
     except ImportError:  # no torch: the binding has yet to be built
         return True
     if not all(os.path.exists(f) for f in built):
@@ -94,14 +99,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if not force and not ptxas_info and not needs_build():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
-    sources = COMMON + SOURCES + MX_SOURCES
+    sources = COMMON + SOURCES + MX_SOURCES + FF_SOURCES
     with cf.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
         bind = ex.submit(_build_bind, verbose)
         objs = dict(zip(sources, ex.map(lambda s: _compile(s, ptxas_info, verbose), sources)))
-    # only the extern "C" API is exported: gemm_* of libttc05, mx_* of libttcmx
+        ff = ex.submit(_link_library, FF_LIB, [objs[s] for s in COMMON + FF_SOURCES], "ff_*",
+                       verbose)
+    # only the extern "C" API is exported: gemm_* of libttc05, mx_* of libttcmx, ff_* of libttcff
     _link(MX_LIB, [objs[s] for s in COMMON + MX_SOURCES], "mx_*", verbose)
     _link(LIB, [objs[s] for s in COMMON + SOURCES], "gemm_*", verbose)
     bind.result()  # needs g++ and torch's headers, which the libraries do not
+    ff.result()
     return LIB
 
 
@@ -121,17 +129,21 @@ def _build_bind(verbose: bool) -> None:
            "-I", sysconfig.get_paths()["include"], "-I", cuda]
     for d in cpp_extension.include_paths():
         cmd += ["-I", d]
-    cmd += [os.path.join(CSRC, BIND_SOURCE), "-o", tmp, "-L", lib_dir, f"-Wl,-rpath,{lib_dir}",
+    cmd += [os.path.join(CSRC, f) for f in BIND_SOURCES] + ["-o", tmp, "-L", lib_dir, f"-Wl,-rpath,{lib_dir}",
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {BIND_SOURCES}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, bind)
 
 
 def _link(lib: str, objs: list, exports: str, verbose: bool) -> None:
+    _link_library(lib, objs, exports, verbose)
+
+
+def _link_library(lib: str, objs: list, exports: str, verbose: bool) -> None:
     tmp = lib + f".tmp{os.getpid()}"
     vs = os.path.join(BUILD_DIR, os.path.basename(lib) + ".map")
     with open(vs, "w") as f:

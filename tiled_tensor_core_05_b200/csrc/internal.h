@@ -113,6 +113,11 @@ int encode_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64
 // swizzle; the innermost coordinate is always 0.
 int encode_tmap_scales(CUtensorMap* map, const void* base, uint64_t tiles, uint32_t box_tiles);
 
+// A matrix of 8- or 16-bit elements (`bytes` 1 or 2) without swizzle: boxes of
+// box_inner elements by box_outer rows, one row after the other; `ld` in elements.
+int encode_tmap_rows(CUtensorMap* map, const void* base, int bytes, uint64_t inner, uint64_t outer,
+                     uint64_t ld, uint32_t box_inner, uint32_t box_outer);
+
 // Large-shape path: persistent warp-specialised tcgen05 kernel, one SM per
 // 128 x block_n tile (GEMM_PATH_TILE), or a pair of SMs per 256 x 256
 // (GEMM_PATH_TILE_PAIR) or 512 x 256 (GEMM_PATH_TILE_PAIR_TALL) tile
