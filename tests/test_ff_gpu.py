@@ -615,7 +615,8 @@ def test_library_refuses_what_the_binding_cannot_see():
 
     assert gated(p, p, p, o) == 0
     assert gated(host, p, p, o) == -1 and gated(p, p, p, host) == -1 and gated(n, p, p, o) == -1
-    assert gated(p, p, p, o, M=1 << 20) == -1 and gated(p, p, p, o, ld=60) == -1
+    # (137 GB of rows: more than any segment that the allocator may have put x into)
+    assert gated(p, p, p, o, M=1 << 30) == -1 and gated(p, p, p, o, ld=60) == -1
     assert gated(p, p, p, o, ld=68) == -2 and gated(p, p, p, o, ldh=1 << 40) == -1
     assert gated(p, p, p, o, M=(1 << 31) - 300, ld=1 << 38) == -1  # wraps in 64 bits
     assert gated(p, p, p, o, G=ctypes.c_void_p(x.data_ptr() + (1 << 19))) == -1  # gate without up
