@@ -384,6 +384,70 @@ def test_w4_special_values(M, dtype):
     assert got[M - 1].isnan().all() and torch.equal(got[:M - 1], base[:M - 1])
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M", [1, 4, 8, 9, 64])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_w4_infinities(M, zeros, dtype):
+    """Infinities in x: what their codes make of them, in their rows alone."""
+    t = DTYPES[dtype]
+    g = gen("w4 infinities", M, zeros)
+    N, K = 77, 600
+    x = normal(g, t, M, K)
+    w, u = (W4(g, N, K, 64, zeros, t) for _ in range(2))
+    base = ttc.gemm_w4(dev(x, t), w.w).cpu()
+    x[M - 1, 130] = float("inf")
+    want = x[M - 1:] @ w.value.t()  # +-infinity, NaN where the weight is 0
+    got = ttc.gemm_w4(dev(x, t), w.w).cpu()
+    assert torch.equal(got[:M - 1], base[:M - 1])
+    assert torch.equal(got[M - 1:].double().nan_to_num(7.0), want.nan_to_num(7.0))
+    assert want.isinf().any()
+    want = want.clamp(min=0).nan_to_num(0.0, posinf=float("inf")) * (x[M - 1:] @ u.value.t())  # ReLU of NaN: 0
+    got = ttc.gemm_gated_w4(dev(x, t), w.w, u.w, "relu").cpu()[M - 1:].double()
+    assert torch.equal(got.isinf(), want.isinf()) and torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got[got.isinf()], want[want.isinf()])
+    x[M - 1, 131] = float("nan")
+    assert ttc.gemm_w4(dev(x, t), w.w).cpu()[M - 1].isnan().all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 20000, 300), (8, 30011, 264), (3, 2400, 9000),
+                                   (8, 40000, 4104)])
+def test_w4_many_tiles(M, N, K):
+    """More tiles than SMs, and than a CTA holds sums of at a time."""
+    t = torch.bfloat16
+    g = gen("tiles", M, N, K)
+    w = W4(g, N, K, 128, True, t)
+    x = integers(g, -1, 1, M, K)
+    bias = integers(g, -8, 8, N)
+    got = ttc.gemm_w4(dev(x, t), w.w, bias.to(t).cuda())
+    ref.close(got, *ref.w4_bound(x, w.value, bias, "none", t))
+
+
+@pytest.mark.parametrize("M", [1, 8])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_w4_range_of_x(M, dtype):
+    """Groups of x at both ends of the type's range, and with values far apart."""
+    t = DTYPES[dtype]
+    g = gen("range", M)
+    N, K = 40, 512
+    # (bf16: as far as sums and what they are rounded to stay normal numbers)
+    lo, hi = (-14, 10) if t is torch.float16 else (-90, 90)
+    x = normal(g, t, M, K) * 2.0 ** torch.randint(lo, hi, (M, K // 32), generator=g).double() \
+        .repeat_interleave(32, 1)
+    x = x.to(t).double()
+    w = W4(g, N, K, 32, True, t)
+    # codes and zero points may be summed apart: magnitudes count both
+    both = ref.weight(w.codes, w.scales.abs(), -w.zeros, 32)
+    for group in range(K // 32):
+        part = torch.zeros_like(x)
+        at = slice(32 * group, 32 * group + 32)
+        part[:, at] = x[:, at]
+        for y in (part, x) if group == 0 else (part,):
+            want, r = y @ w.value.t(), ref.HALF[t]
+            off = ref.sum_bound(32 if y is part else K, y.abs() @ both.t())
+            ref.close(ttc.gemm_w4(dev(y, t), w.w), want,
+                      off * (1 + r) + r * want.abs() + ref.TINY[t])
+
+
 def test_w4_slices_of_rows():
     """Rows of a weight are a weight."""
     t = torch.float16

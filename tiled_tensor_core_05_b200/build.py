@@ -32,9 +32,11 @@ COMMON = ["host_common.cu"]  # linked into every library
 SOURCES = ["gemm_api.cu", "gemm_tile.cu", "gemm_skinny.cu", "gemm_skinny_even.cu", "gemm_host.cu"]
 MX_SOURCES = ["mx_api.cu", "mx_rows.cu", "mx_gemm_split.cu", "mx_gemm_pair.cu",
               "mx_gemm_pair_split.cu"]
-FF_SOURCES = ["ff_api.cu", "ff_pair.cu", "ff_split.cu", "ff_rows.cu", "ff_w4.cu"]
+FF_SOURCES = ["ff_api.cu", "ff_pair.cu", "ff_split.cu", "ff_rows.cu", "ff_w4.cu",
+              "ff_w4_few.cu"]
 HEADERS = ["sm100.cuh", "extent.h", "internal.h", "skinny_common.cuh", "tile_common.cuh",
            "mx_internal.h", "mx_common.cuh", "mx_umma.cuh", "ff_internal.h", "ff_common.cuh",
+           "ff_w4.cuh",
            "bind_common.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -65,6 +65,9 @@ int launch_pair_product(const Product& p, const DeviceCtx& d);
 int launch_split_product(const Product& p, const DeviceCtx& d);
 int launch_slope(const SlopeProblem& p, const DeviceCtx& d);
 int launch_w4(const W4Problem& p, const DeviceCtx& d);
+// The kernel of launch_w4 for very few rows, and whether it takes a product.
+bool w4_few_fits(const W4Problem& p);
+int launch_w4_few(const W4Problem& p, const DeviceCtx& d);
 // Y = act(bias) (act(0) without one): products over no elements
 int launch_bias_fill(const void* bias, void* Y, int64_t rows, int64_t cols, int64_t ldy, int dtype,
                      int act, cudaStream_t stream);

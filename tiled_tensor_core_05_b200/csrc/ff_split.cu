@@ -257,7 +257,7 @@ int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   for (int c = 2; c <= kMaxSplits && stages >= 4 * c; ++c) {
     const int n =
         residency[d.device & 63].of(c, ff_split_kernel<BN, DEEP>, kThreads, C::kSmemBytes, d);
-    if (tiles <= static_cast<int64_t>(n) * C::kPerSm) splits = c;
+    if (tiles <= n) splits = c;
   }
   return splits;
 }

@@ -18,7 +18,7 @@
 //   warp 9     tcgen05.mma, A from TMEM (two buffers), B (x) from shared memory
 #include <atomic>
 
-#include "ff_common.cuh"
+#include "ff_w4.cuh"
 
 namespace ttc {
 namespace ff {
@@ -130,42 +130,6 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
   tmem_load_32x32b_x32(taddr, r);
-}
-
-// A zero point as what dequantize8 subtracts, twice in a word: of 1024 + code (fp16)
-// or 128 + code (bf16), the numbers whose last mantissa bits are the code.
-template <class T>
-__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
-  return (z | (std::is_same<T, __half>::value ? 0x6400u : 0x4300u)) * 0x10001u;
-}
-
-// The 8 codes of a word minus the zero point, in pairs of neighbours.
-template <class T>
-__device__ __forceinline__ void dequantize8(uint32_t w, uint32_t zero, uint32_t* p) {
-  if constexpr (std::is_same<T, __half>::value) {
-    // bits 4 .. 7 of a half hold 16 times the code: 1024 + 16 code, divided by 16
-    // and minus 64 + zero in one fused step (all exact)
-    const __half2 z = *reinterpret_cast<const __half2*>(&zero);
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
-    const __half2 z64 = __hsub2(__float2half2_rn(960.0f), z);  // -(64 + zero)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t v = w >> (8 * i);
-      const uint32_t lo = (v & 0x000F000Fu) | 0x64006400u, hi = (v & 0x00F000F0u) | 0x64006400u;
-      const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), z);
-      const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), sixteenth, z64);
-      p[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
-      p[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-  } else {
-    const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162*>(&zero);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-      const __nv_bfloat162 a = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), z);
-      p[i] = *reinterpret_cast<const uint32_t*>(&a);
-    }
-  }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -470,7 +434,7 @@ int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   for (int c = 2; c <= kMaxSplits && stages >= 2 * c; ++c) {
     const int n =
         residency[d.device & 63].of(c, ff_w4_kernel<T, BN, GROUP>, kThreads, C::kSmemBytes, d);
-    if (tiles <= static_cast<int64_t>(n) * C::kPerSm) splits = c;
+    if (tiles <= n) splits = c;
   }
   return splits;
 }
@@ -560,6 +524,7 @@ int launch_group(const W4Problem& p, const DeviceCtx& d) {
 }  // namespace
 
 int launch_w4(const W4Problem& p, const DeviceCtx& d) {
+  if (w4_few_fits(p)) return launch_w4_few(p, d);
   return p.dtype == MX_F16 ? launch_group<__half>(p, d) : launch_group<__nv_bfloat16>(p, d);
 }
 
