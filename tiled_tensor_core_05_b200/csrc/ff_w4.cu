@@ -425,7 +425,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, GROUP>::kPerSm)
   }
 }
 
-// Into how many parts of at least two stages K is divided: as many as run in one wave.
+// Into how many parts of at least two stages K is divided: as many as run in one wave (16 x
+// 14336 x 4096 16.9 us in 2 parts, which share SMs, and 24.9 in 1; 16 x 8192 x 8192 18.2 and
+// 27.5 with half the CTAs).  More than a wave is slower, although the 224 tiles of 16 x 28672 x
+// 8192 leave 72 of 148 SMs with one CTA instead of two: 52.8 us, 55.6 in 2 parts, 57.0 in 3.
 template <class T, int BN, int GROUP>
 int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   using C = Cfg<BN, GROUP>;
@@ -434,7 +437,7 @@ int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   for (int c = 2; c <= kMaxSplits && stages >= 2 * c; ++c) {
     const int n =
         residency[d.device & 63].of(c, ff_w4_kernel<T, BN, GROUP>, kThreads, C::kSmemBytes, d);
-    if (tiles <= n) splits = c;
+    if (tiles <= static_cast<int64_t>(n) * C::kPerSm) splits = c;
   }
   return splits;
 }
