@@ -247,8 +247,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Into how many parts of at least four k-blocks K is divided: as many as run in
-// one wave.
+// Into how many parts of at least four k-blocks K is divided: as many as run in one wave
+// with a CTA an SM.  (Counting two an SM: 16 and 64 x 4096 -> 14336, gated, 39.9 and 41.2 us
+// instead of 37.9 and 39.4; dX of 64 x 4096 <- 4096 2 us faster, of 8192 <- 8192 the same.)
 template <int BN, bool DEEP>
 int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
   using C = Cfg<BN, DEEP>;

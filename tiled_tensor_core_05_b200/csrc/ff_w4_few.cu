@@ -35,7 +35,9 @@
 // with the weights brought by cp.async, whose addresses and edges cost as many instructions
 // as the products, they took 16.5, 26.2 and 43.1 us.  12 warps: 12.5, 21.5, 31.1 us; 20:
 // 12.6, 20.4, 28.0; 24: 13.7, 21.3, 29.1; 3 blocks on their way instead of 2: 12.2, 20.3,
-// 28.9, and fewer rows fit.
+// 28.9, and fewer rows fit.  16 rows with K divided among a cluster of 4, so that x fits,
+// took 125 us, the kernel of more rows 53: sums of 16 warps and rows hold few tiles at a
+// time, and everything waits at the end of each few.
 #include <atomic>
 
 #include "ff_w4.cuh"
@@ -50,7 +52,7 @@ constexpr int kBlockK = 256;  // columns of a block
 constexpr int kRows = 8;      // of x
 constexpr int kTileRows = 16;
 constexpr int kXBatch = 4;    // blocks of x that a warp asks for at a time
-constexpr int kDepth = 2;     // blocks of a warp on their way
+constexpr int kDepth = 2;  // blocks of a warp on their way
 
 // A place of a ring: a block's codes, [half][row], 128-byte swizzled; and elsewhere
 // its groups' scales and zero points, [group][row], for each half (gated) or both.
@@ -492,7 +494,8 @@ int launch_group(const W4Problem& p, const DeviceCtx& d) {
 
 }  // namespace
 
-// Up to 8 rows, as long as they fit into shared memory beside the rings.
+// Up to 8 rows, as long as they fit into shared memory beside the rings (8 x 14336 x 4096
+// 16.1 us; the kernel of more rows takes 17 for 16 of them; 1 x 14336 x 4096 12.1 and 16.4).
 bool w4_few_fits(const W4Problem& p) {
   if (p.M > kRows) return false;
   const int64_t base = p.group == 32   ? base_bytes<32>(p.M, p.K)
