@@ -205,3 +205,12 @@ def test_weight_by_hand(group):
             i = k // group
             assert w[n, k] == (k % 16 - (2 * i + n) % 16) * (2 * i + n + 1)
     assert ref.weight(codes, scales, None, group)[1, 5] == (5 - 8) * 2
+
+
+def test_parts_of_a_weight_cannot_be_exchanged(ttc):
+    """A product takes the tensors that were checked: another one in their place is refused."""
+    w = ttc.w4_pack(torch.zeros(16, 64, dtype=torch.uint8), torch.ones(16, 1).half(), group=64)
+    for name in ("data", "scales", "zeros"):
+        with pytest.raises(AttributeError):
+            setattr(w, name, getattr(w, name))
+    assert w.data.shape == (16, 32) and w.scales.shape == (1, 16) and w.zeros is None

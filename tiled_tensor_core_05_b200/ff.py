@@ -129,7 +129,7 @@ class W4Tensor:
     Rows of scales and zeros start on 16 bytes, too.  A slice of rows (of multiples of 16) is a
     weight again: of data[a:b], scales[:, a:b], zeros[:, a:b]."""
 
-    __slots__ = ("data", "scales", "zeros", "rows", "cols", "group", "_args")
+    __slots__ = ("rows", "cols", "group", "_args")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None,
                  rows: int, cols: int, group: int):
@@ -162,9 +162,13 @@ class W4Tensor:
             elif step % unit:
                 raise ValueError(f"the rows of {what} must start on 16 bytes")
             strides.append(step)
-        self.data, self.scales, self.zeros = data, scales, zeros
         self.rows, self.cols, self.group = rows, cols, group
         self._args = (data, scales, zeros, *strides)
+
+    # (read-only: what the products take was checked together with its strides)
+    data = property(lambda self: self._args[0])
+    scales = property(lambda self: self._args[1])
+    zeros = property(lambda self: self._args[2])
 
     @property
     def shape(self) -> tuple[int, int]:
@@ -235,7 +239,7 @@ def gemm_w4(x: torch.Tensor, w: W4Tensor, bias: torch.Tensor | None = None,
             act: str | int = "none", out: torch.Tensor | None = None, *,
             stream=None) -> torch.Tensor:
     """y = act(x @ W.T + bias) for few rows of ``x`` (M, K), fp16 or bf16 as the scales of ``w``
-    are; ``bias`` N values or None; ``act`` "none" / "relu" / "gelu" / "silu".  Codes minus zero
+    are; ``bias`` N values or None; ``act`` "none" / "relu" / "gelu" / "silu".  Codes and zero
     points are exact and sums are fp32: no weight is rounded.  The weight is read once for every
     64 rows."""
     _check_w4(w, "w", x)
