@@ -71,8 +71,9 @@ GEMM_API int ff_gated_backward(const void* dH, const void* X, const void* Wg, co
  *      bytes (a multiple of 16), or NULL: 8 for all.
  *
  * Y = act(X W^T + bias).  X: M x K, Y: M x N, bias: N values or NULL, of type dtype.
- * Code minus zero is exact in 16 bits, the sums of a group are fp32 and take its
- * scale there: no weight is rounded.  Made for few rows: a weight is read once for
+ * Codes and zero points are exact, the sums of a group are fp32 and take its scale
+ * there: no weight is rounded.  (With up to 8 rows a group's codes and its zero point
+ * are summed apart, so that an fp32 sum's error counts code + zero, not their difference.)  Made for few rows: a weight is read once for
  * every 64 of them.  K == 0 gives act(bias). */
 GEMM_API int ff_w4_gemm(const void* X, const void* Q, const void* S, const void* Z,
                         const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int64_t ldx,
