@@ -216,7 +216,9 @@ __device__ __forceinline__ void join_and_finish(const Tail& o, uint8_t* part, ui
   } else {
     __syncthreads();
   }
-  const bool aborted = *abort_flag != 0;
+  // (one answer a warp: a wait that runs out may have ended well for some of its lanes, and
+  // finish_rows exchanges sums between all of them)
+  const bool aborted = __any_sync(0xffffffffu, *abort_flag != 0);
   if (splits > 1 && pull) {
     static_assert(kPullRows * 16 <= kThreads, "a row for 16 threads");
     float v[8] = {};
