@@ -448,6 +448,62 @@ def test_w4_range_of_x(M, dtype):
                       off * (1 + r) + r * want.abs() + ref.TINY[t])
 
 
+@pytest.mark.parametrize("M", [1, 5, 8])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_small_bf16_results(M, group):
+    """Few rows whose results go down to bf16's subnormals keep bf16's bits."""
+    t = torch.bfloat16
+    g = gen("small", M, group)
+    N, K = 70, 512
+    w = W4(g, N, K, group, True, t)
+    both = ref.weight(w.codes, w.scales.abs(), -w.zeros, group)
+    for exponent in (-104, -110, -116, -122, -128):
+        x = (torch.randn(M, K, generator=g).double() * 2.0 ** exponent).to(t).double()
+        want, r = x @ w.value.t(), ref.HALF[t]
+        # fp32 results below 2^-126 are off by up to 2^-150 each: 3 for each of up to 16 groups and
+        # 16 more for joining them, all in terms of the result or of it by a scale below 1
+        assert w.scales.abs().max() < 1
+        off = ref.sum_bound(K, x.abs() @ both.t()) + 64 * 2.0 ** -150
+        ref.close(ttc.gemm_w4(dev(x, t), w.w), want, off * (1 + r) + r * want.abs() + ref.TINY[t],
+                  f"2^{exponent}")
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M", [1, 8])
+@pytest.mark.parametrize("group", [32, 128])
+def test_w4_large_bf16_values(M, group, zeros):
+    """Values of x close to bf16's largest, in their rows alone; a code at its zero point takes
+    them out of a result."""
+    t = torch.bfloat16
+    g = gen("large", M, group, zeros)
+    N, K = 90, 400
+    x = normal(g, t, M, K)
+    w = W4(g, N, K, group, zeros, t)
+    base = ttc.gemm_w4(dev(x, t), w.w).cpu()
+    for exponent in (117, 118, 119, 122):
+        x[M - 1, 133] = 2.0 ** exponent
+        want, r = x @ w.value.t(), ref.HALF[t]
+        assert want.abs().max() < 2.0 ** 127
+        got = ttc.gemm_w4(dev(x, t), w.w).cpu()
+        assert torch.equal(got[:M - 1], base[:M - 1])
+        # summed in one chain of fp32 additions a group, then one of the groups (from 2^118 on; below,
+        # codes and zero points apart, to which a code at its zero point is no exception)
+        if exponent >= 118:
+            off = (group + -(-K // group)) * 2.0 ** -24 * (x.abs() @ w.value.abs().t())
+        else:
+            both = ref.weight(w.codes, w.scales.abs(), -w.zeros if zeros else
+                              torch.full(w.scales.shape, -8), group)
+            off = ref.sum_bound(K, x.abs() @ both.t())
+            # x is held to 2^-35 of the largest value of its group
+            at = slice(133 // group * group, 133 // group * group + group)
+            steps = w.codes[:, at].double().sum(1) * w.scales[133 // group].abs()
+            off[M - 1] += 2.0 ** (exponent - 35) * steps
+        ref.close(got[M - 1:], want[M - 1:],
+                  (off * (1 + r) + r * want.abs() + ref.TINY[t])[M - 1:], f"2^{exponent}")
+    # (a column whose code is its zero point was among them)
+    assert exponent >= 118 and (want[M - 1].abs() < 2.0 ** 20).any()
+
+
 def test_w4_slices_of_rows():
     """Rows of a weight are a weight."""
     t = torch.float16

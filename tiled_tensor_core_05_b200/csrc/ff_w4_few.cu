@@ -8,11 +8,14 @@
 // code 2^-20.  The tensor cores multiply these exactly.  Four masks and a shift make
 // the operands of 8 codes.  x is prepared for that once a CTA: each row, a group of
 // columns at a time, as
-//     x = e y,  e = 2^(floor(log2 max |x|) - 14),
+//     x = e 2^-24 y,  e = 2^(floor(log2 max |x|) + 10),
 // y in fp16 (a sixteenth of it for the columns whose codes lie in the upper bits): exactly,
 // but for what lies below 2^-34 of the group's largest value.  Then, in fp32,
-//     sum (code - zero) x = e 2^24 (sum (code 2^-24) y - zero sum 2^-24 y),
-// and the group's scale is applied to that: no weight is rounded.
+//     sum (code - zero) x = e (sum (code 2^-24) y - zero sum 2^-24 y),
+// and the group's scale is applied to that: no weight is rounded.  (The scale comes last, so
+// that fp32 holds the group's sum itself, not a part of 2^24 of it: bf16 results keep their bits
+// down to bf16's smallest.)  Rows of x with infinities or with values of 2^118 and more, whose e
+// fp32 cannot hold, are summed plainly.
 //
 // A CTA an SM goes through its tiles of 16 rows of the weights (gated: 8 of each); its
 // warps take the tiles' blocks of 256 columns in turn, each with its own ring in shared
@@ -98,6 +101,9 @@ __device__ __forceinline__ void mma16816(float2 (&d)[2], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The bits of 2^118: from there on a row is summed plainly.
+constexpr uint32_t kPlainFrom = (127u + 118u) << 23;
+
 // y, e and the sums of y of a row's block, 8 columns a lane.  bits: of the group's largest
 // magnitude; a NaN's or an infinity's is above all others.
 template <class T, int GROUP>
@@ -109,8 +115,9 @@ __device__ __forceinline__ uint4 prepare8(const uint4& raw, uint32_t& bits, floa
   for (int i = 0; i < 8; ++i) bits = max(bits, __float_as_uint(fabsf(v[i])));
 #pragma unroll
   for (int o = 1; o < GROUP / 8; o <<= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
-  // floor(log2) + 127, at least 27 (smaller bf16 values become multiples of 2^-138), so that
-  // both powers are normal numbers
+  // floor(log2) + 127, at least 27 (y of smaller groups loses nothing: bf16's subnormals are
+  // multiples of 2^-133, a sixteenth of y holds those of 2^-134), so that both powers are normal
+  // numbers
   const uint32_t field = min(max(bits >> 23, 27u), 254u);
   const float inverse = __uint_as_float((268u - field) << 23);
   sum = 0.0f;
@@ -123,7 +130,7 @@ __device__ __forceinline__ uint4 prepare8(const uint4& raw, uint32_t& bits, floa
   for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   sum *= 5.9604644775390625e-8f;  // 2^-24
   // NaN: the row's sums become NaN
-  e = __uint_as_float(bits >= 0x7F800000u ? 0x7FC00000u : (field - 14u) << 23);
+  e = __uint_as_float(bits >= kPlainFrom ? 0x7FC00000u : (field + 10u) << 23);
   v[2] *= 0.0625f;
   v[3] *= 0.0625f;
   v[6] *= 0.0625f;
@@ -131,8 +138,8 @@ __device__ __forceinline__ uint4 prepare8(const uint4& raw, uint32_t& bits, floa
   return mx::pack8<__half>(v);
 }
 
-// The sum of a row of x and a row of a weight times 2^-24, as the kernel's are: for rows
-// with infinities, which its split into e and y cannot hold.
+// The sum of a row of x times a row of a weight, for rows that the split into e and y cannot
+// hold.
 template <class T, int GROUP>
 __device__ __noinline__ float plain_sum(const uint16_t* x, const W4Weight& w, int n, int K) {
   const uint8_t* q = static_cast<const uint8_t*>(w.Q) + n * w.ldq;
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* codes = smem + warp * (kDepth * kCodes);
   uint8_t* scales = smem + kWarps * kDepth * kCodes + warp * (kDepth * kScales);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes) + warp * kDepth;
-  // bits m and 8 + m: row m of x holds an infinity, a NaN
+  // bits m and 8 + m: row m of x holds an infinity or what is as large as kPlainFrom, a NaN
   int* special = reinterpret_cast<int*>(smem + kRingBytes + kWarps * kDepth * 8);
   volatile int* abort_flag = special + 1;
   uint8_t* smX = smem + kRingBytes + kWarps * kDepth * 8 + 16;  // [row][block] y
@@ -265,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   ((block * kGroups + lane / (4 * VEC)) * pairs + (row >> 1)) * 4 + (row & 1);
       at[0] = e;
       at[2] = sum;
-      if (bits >= 0x7F800000u) atomicOr(special, (bits == 0x7F800000u ? 1 : 256) << row);
+      if (bits >= kPlainFrom) atomicOr(special, (bits <= 0x7F800000u ? 1 : 256) << row);
     }
   };
   for (int i = warp; i < M * blocks; i += kXBatch * kWarps) {
@@ -294,8 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.z += p.z;
       s.w += p.w;
     }
-    constexpr float kCode = 16777216.0f;  // 2^24
-    s = make_float4(s.x * kCode, s.y * kCode, s.z * kCode, s.w * kCode);
     const int n = tile * kTileN + row, m = 2 * t;
     if (*special != 0) {
       auto again = [&](int i, int w, int col, float v) {
@@ -401,8 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               acc[h] = __ffma2_rn(
-                  __fmul2_rn(make_float2(scale[h], scale[h]), make_float2(e.x, e.y)),
-                  __ffma2_rn(make_float2(-zero[h], -zero[h]), make_float2(e.z, e.w), sum[h]),
+                  make_float2(scale[h], scale[h]),
+                  __fmul2_rn(make_float2(e.x, e.y),
+                             __ffma2_rn(make_float2(-zero[h], -zero[h]), make_float2(e.z, e.w),
+                                        sum[h])),
                   acc[h]);
           }
           __syncwarp();
