@@ -721,6 +721,45 @@ def test_refusals():
     assert (ttc.gemm_w4(x, q) == 0).all() and ttc.ff_device_status() == 0
 
 
+def test_gradients_are_not_lost_in_silence():
+    """A backward pass through a result without a graph raises; calls without one are as before."""
+    t = torch.float16
+    g = gen("no graph")
+    x, wg, wu = (dev(normal(g, t, *s), t) for s in ((4, 64), (16, 64), (16, 64)))
+    w = W4(g, 16, 64, 64, False, t).w
+    b = torch.ones(16, dtype=t, device="cuda")
+    h, y, z = ttc.gemm_gated(x, wg, wu), ttc.gemm_w4(x, w, b), ttc.gemm_gated_w4(x, w, w)
+    assert not (h.requires_grad or y.requires_grad or z.requires_grad)
+
+    def leaf(v):
+        return v.detach().requires_grad_()
+
+    calls = [(h, lambda **k: ttc.gemm_gated(leaf(x), wg, wu, **k), "gemm_gated_backward"),
+             (h, lambda **k: ttc.gemm_gated(x, leaf(wg), wu, **k), "gemm_gated_backward"),
+             (h, lambda **k: ttc.gemm_gated(x, wg, leaf(wu), **k), "gemm_gated_backward"),
+             (y, lambda **k: ttc.gemm_w4(leaf(x), w, b, **k), "gemm_w4 has no"),
+             (y, lambda **k: ttc.gemm_w4(x, w, leaf(b), **k), "gemm_w4 has no"),
+             (z, lambda **k: ttc.gemm_gated_w4(leaf(x), w, w, **k), "gemm_gated_w4 has no")]
+    for want, call, message in calls:
+        got = call()
+        assert torch.equal(got.detach(), want) and got.requires_grad
+        with pytest.raises(RuntimeError, match=message):
+            got.float().sum().backward()
+        out = torch.zeros_like(want)
+        with pytest.raises(RuntimeError, match=message):
+            call(out=out)
+        assert (out == 0).all()
+        with torch.no_grad():
+            assert call(out=out) is out and torch.equal(out, want)
+            assert not call().requires_grad
+    # with save the gradients are the caller's own business
+    results = ttc.gemm_gated(leaf(x), leaf(wg), leaf(wu), save=True)
+    assert torch.equal(results[0], h) and not any(v.requires_grad for v in results)
+    results[0].requires_grad_().float().sum().backward()
+    grads = ttc.gemm_gated_backward(results[0].grad, leaf(x), leaf(wg), leaf(wu), *results[1:])
+    assert not any(v.requires_grad for v in grads)
+
+
 def test_library_refuses_what_the_binding_cannot_see():
     """Through the C boundary: extents past the allocation, host pointers, too large strides."""
     import ctypes

@@ -4,6 +4,9 @@
 #include "../../include/gemm_ff.h"
 #include "bind_common.h"
 
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
+
 namespace {
 
 struct Entry {
@@ -46,6 +49,24 @@ struct Input {  // a matrix of activations and what follows from it
   }
 };
 
+// These operators record no graph.  Where an input requires a gradient, a backward pass that
+// reaches their result raises `message`: without it the gradient would be lost in silence.
+// As with torch's own out= forms, a given result (`out`) is refused then, before anything runs.
+struct NoGraph {
+  std::shared_ptr<torch::autograd::Node> node;
+  template <class... Inputs>
+  NoGraph(PyObject* out, const char* message, const Inputs&... inputs) {
+    if (!torch::autograd::compute_requires_grad(inputs...)) return;
+    if (out != Py_None)
+      fail(PyExc_RuntimeError, "out= is for inputs that require no gradient: %s", message);
+    node = std::make_shared<torch::autograd::Error>(
+        message, torch::autograd::collect_next_edges(inputs...));
+  }
+  void mark(const at::Tensor& result) const {
+    if (node) torch::autograd::set_history(result, node);
+  }
+};
+
 int64_t rows_of(const at::Tensor& t, const char* what) {
   if (t.dim() != 2) fail(PyExc_ValueError, "%s must be a matrix", what);
   return t.size(0);
@@ -60,13 +81,19 @@ PyObject* gated(PyObject* const* a, Py_ssize_t n) {
   const Mat mg(wg, "w_gate", F, x.cols, x.type, x.device);
   const Mat mu(wu, "w_up", F, x.cols, x.type, x.device);
   const int act = static_cast<int>(integer(a[3]));
+  const bool save = a[5] == Py_True;
+  // (with save the caller takes the gradients)
+  const NoGraph no_graph(save ? Py_None : a[4],
+                         "gemm_gated records no graph: call it with save=True and take the "
+                         "gradients from gemm_gated_backward",
+                         x.t, wg, wu);
   Context c(x.device, a[6]);
   const at::Tensor h =
       a[4] != Py_None ? tensor(a[4], "out") : new_matrix(x.rows, F, x.type, x.device);
   const Mat mh(h, "out", x.rows, F, x.type, x.device);
   at::Tensor gate, up;
   Mat sg, su;
-  if (a[5] == Py_True) {
+  if (save) {
     gate = new_matrix(x.rows, F, at::kFloat, x.device);
     up = new_matrix(x.rows, F, at::kFloat, x.device);
     sg = Mat(gate, "gate", x.rows, F, at::kFloat, x.device);
@@ -76,6 +103,7 @@ PyObject* gated(PyObject* const* a, Py_ssize_t n) {
     return g_entry.gated(x.m.p, mg.p, mu.p, mh.p, sg.p, su.p, x.rows, F, x.cols, x.m.ld, mg.ld,
                          mu.ld, mh.ld, sg.ld, su.ld, x.dtype, act, c.handle());
   });
+  if (!save) no_graph.mark(h);
   return Py_BuildValue("iNNN", rc, wrap(h), wrap_or_none(gate), wrap_or_none(up));
 }
 
@@ -140,8 +168,10 @@ PyObject* w4_gemm(PyObject* const* a, Py_ssize_t n) {
   const Weight w(a + 1, x);
   const int64_t N = integer(a[7]);
   const int group = static_cast<int>(integer(a[8])), act = static_cast<int>(integer(a[10]));
-  const void* bias = a[9] == Py_None ? nullptr
-                                     : vector(tensor(a[9], "bias"), "bias", N, x.type, x.device);
+  const at::Tensor bias_t = a[9] == Py_None ? at::Tensor() : tensor(a[9], "bias");
+  const void* bias =
+      bias_t.defined() ? vector(bias_t, "bias", N, x.type, x.device) : nullptr;
+  const NoGraph no_graph(a[11], "gemm_w4 has no backward pass", x.t, bias_t);
   Context c(x.device, a[12]);
   const at::Tensor y =
       a[11] != Py_None ? tensor(a[11], "out") : new_matrix(x.rows, N, x.type, x.device);
@@ -150,6 +180,7 @@ PyObject* w4_gemm(PyObject* const* a, Py_ssize_t n) {
     return g_entry.w4_gemm(x.m.p, w.q, w.s, w.z, bias, my.p, x.rows, N, x.cols, x.m.ld, w.ldq,
                            w.lds, w.ldz, my.ld, group, x.dtype, act, c.handle());
   });
+  no_graph.mark(y);
   return Py_BuildValue("iN", rc, wrap(y));
 }
 
@@ -160,6 +191,7 @@ PyObject* w4_gated(PyObject* const* a, Py_ssize_t n) {
   const Weight g(a + 1, x), u(a + 7, x);
   const int64_t F = integer(a[13]);
   const int group = static_cast<int>(integer(a[14])), act = static_cast<int>(integer(a[15]));
+  const NoGraph no_graph(a[16], "gemm_gated_w4 has no backward pass", x.t);
   Context c(x.device, a[17]);
   const at::Tensor h =
       a[16] != Py_None ? tensor(a[16], "out") : new_matrix(x.rows, F, x.type, x.device);
@@ -169,6 +201,7 @@ PyObject* w4_gated(PyObject* const* a, Py_ssize_t n) {
                             g.ldq, g.lds, g.ldz, u.ldq, u.lds, u.ldz, mh.ld, group, x.dtype, act,
                             c.handle());
   });
+  no_graph.mark(h);
   return Py_BuildValue("iN", rc, wrap(h));
 }
 

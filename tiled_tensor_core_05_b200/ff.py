@@ -94,7 +94,10 @@ def gemm_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: s
 
     Returns h (M, F) or, with ``save``, (h, gate, up): the two projections in fp32, which
     :func:`gemm_gated_backward` takes (rounded to 16 bits they would put the gradients 1.8 times
-    as far from exact as a single rounding does; in fp32 it is 1.4 times)."""
+    as far from exact as a single rounding does; in fp32 it is 1.4 times).
+
+    No autograd graph is recorded: the results of ``save`` are plain tensors, and a backward pass
+    that reaches h without it, through inputs that require gradients, raises."""
     rc, h, gate, up = (_bind or _loaded()).gated(x, w_gate, w_up, _act(act), out, bool(save),
                                                  _handle(stream))
     if rc:
@@ -241,7 +244,7 @@ def gemm_w4(x: torch.Tensor, w: W4Tensor, bias: torch.Tensor | None = None,
     """y = act(x @ W.T + bias) for few rows of ``x`` (M, K), fp16 or bf16 as the scales of ``w``
     are; ``bias`` N values or None; ``act`` "none" / "relu" / "gelu" / "silu".  Codes and zero
     points are exact and sums are fp32: no weight is rounded.  The weight is read once for every
-    64 rows."""
+    64 rows.  There is no backward pass: one that reaches y raises."""
     _check_w4(w, "w", x)
     rc, y = (_bind or _loaded()).w4_gemm(x, *w._args, w.rows, w.group, bias, _act(act), out,
                                          _handle(stream))
