@@ -214,3 +214,12 @@ def test_parts_of_a_weight_cannot_be_exchanged(ttc):
         with pytest.raises(AttributeError):
             setattr(w, name, getattr(w, name))
     assert w.data.shape == (16, 32) and w.scales.shape == (1, 16) and w.zeros is None
+
+
+@pytest.mark.parametrize("name", ["rows", "cols", "group"])
+def test_sizes_of_a_weight_cannot_be_changed(ttc, name):
+    """They were checked together with the tensors, whose extents the library takes from them."""
+    w = ttc.w4_pack(torch.zeros(16, 64, dtype=torch.uint8), torch.ones(16, 1).half(), group=64)
+    with pytest.raises(AttributeError):
+        setattr(w, name, 2 * getattr(w, name))
+    assert w.shape == (w.rows, w.cols) == (16, 64) and w.group == 64

@@ -132,7 +132,7 @@ class W4Tensor:
     Rows of scales and zeros start on 16 bytes, too.  A slice of rows (of multiples of 16) is a
     weight again: of data[a:b], scales[:, a:b], zeros[:, a:b]."""
 
-    __slots__ = ("rows", "cols", "group", "_args")
+    __slots__ = ("_rows", "_cols", "_group", "_args")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None,
                  rows: int, cols: int, group: int):
@@ -165,10 +165,13 @@ class W4Tensor:
             elif step % unit:
                 raise ValueError(f"the rows of {what} must start on 16 bytes")
             strides.append(step)
-        self.rows, self.cols, self.group = rows, cols, group
+        self._rows, self._cols, self._group = rows, cols, group
         self._args = (data, scales, zeros, *strides)
 
-    # (read-only: what the products take was checked together with its strides)
+    # (read-only: what the products take was checked together)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    group = property(lambda self: self._group)
     data = property(lambda self: self._args[0])
     scales = property(lambda self: self._args[1])
     zeros = property(lambda self: self._args[2])
