@@ -111,6 +111,16 @@ def test_layout_of_codes(ttc, rows, cols):
         assert ttc.w4_pack(codes, scales, group=group).zeros is None
 
 
+@pytest.mark.parametrize("rows,cols", [(0, 0), (0, 64), (5, 0)])
+def test_layout_of_no_codes(ttc, rows, cols):
+    codes = torch.zeros(rows, cols, dtype=torch.uint8)
+    zeros = torch.zeros(rows, -(-cols // 32), dtype=torch.uint8)
+    w = ttc.w4_pack(codes, zeros.half(), zeros, group=32)
+    assert w.shape == (rows, cols) and w.scales.shape == w.zeros.shape == (-(-cols // 32), rows)
+    got = ttc.w4_unpack(w)
+    assert got.dtype == torch.uint8 and got.shape == (rows, cols)
+
+
 def test_word_by_hand():
     """Columns 0 .. 7 of a word: 0, 2, 4, 6 in the low half, 1, 3, 5, 7 in the high half."""
     words = ref.pack_words(torch.arange(8)[None])

@@ -227,9 +227,10 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor,
 
 def w4_unpack(w: W4Tensor) -> torch.Tensor:
     """The codes (rows, cols) of ``w``."""
-    b = w.data[:, :(w.cols + 7) // 8 * 4].reshape(w.rows, -1, 2, 2)  # word, parity, byte
-    c = torch.stack((b & 15, b >> 4), 4)                             # ..., column pair of the byte
-    return c.permute(0, 1, 3, 4, 2).reshape(w.rows, -1)[:, :w.cols]
+    words = (w.cols + 7) // 8
+    b = w.data[:, :words * 4].reshape(w.rows, words, 2, 2)  # word, parity, byte
+    c = torch.stack((b & 15, b >> 4), 4)                    # ..., column pair of the byte
+    return c.permute(0, 1, 3, 4, 2).reshape(w.rows, words * 8)[:, :w.cols]
 
 
 def _check_w4(w: W4Tensor, what: str, x: torch.Tensor) -> None:
