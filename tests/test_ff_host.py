@@ -121,6 +121,17 @@ def test_layout_of_no_codes(ttc, rows, cols):
     assert got.dtype == torch.uint8 and got.shape == (rows, cols)
 
 
+@pytest.mark.parametrize("rows,groups", [(16, 1), (1, 1), (1, 4), (16, 2), (5, 1)])
+def test_packed_weight_is_its_own(ttc, rows, groups):
+    """What happens to the codes, scales and zero points afterwards does not reach the weight."""
+    codes = torch.full((rows, 32 * groups), 3, dtype=torch.uint8)
+    scales, zeros = torch.ones(rows, groups).half(), torch.full((rows, groups), 7).byte()
+    w = ttc.w4_pack(codes, scales, zeros, group=32)
+    for t in (codes, scales, zeros):
+        t.fill_(9)
+    assert (ttc.w4_unpack(w) == 3).all() and (w.scales == 1).all() and (w.zeros == 7).all()
+
+
 def test_word_by_hand():
     """Columns 0 .. 7 of a word: 0, 2, 4, 6 in the low half, 1, 3, 5, 7 in the high half."""
     words = ref.pack_words(torch.arange(8)[None])

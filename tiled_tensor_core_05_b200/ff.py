@@ -190,11 +190,9 @@ class W4Tensor:
 
 
 def _rows_on_16(t: torch.Tensor) -> torch.Tensor:
-    """t with rows that start on 16 bytes: t itself where they do."""
+    """A copy of t whose rows start on 16 bytes."""
     unit = 16 // t.element_size()
     rows, cols = t.shape
-    if t.stride(1) == 1 and (rows <= 1 or t.stride(0) % unit == 0) and t.data_ptr() % 16 == 0:
-        return t
     buf = torch.empty((rows, -(-cols // unit) * unit), dtype=t.dtype, device=t.device)
     buf[:, :cols] = t
     return buf[:, :cols]
@@ -204,7 +202,7 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor,
             zeros: torch.Tensor | None = None, *, group: int = 128) -> W4Tensor:
     """The weight of ``codes`` (rows, cols) uint8 0 .. 15, ``scales`` (rows, groups) fp16 or bf16 and
     ``zeros`` (rows, groups) uint8 0 .. 15 or None (8 for all), on their device.  Done once, when a
-    model is loaded."""
+    model is loaded; the weight keeps nothing of its arguments."""
     if codes.dtype is not torch.uint8 or codes.dim() != 2:
         raise TypeError("codes must be a matrix of torch.uint8")
     if group not in GROUPS:
