@@ -721,6 +721,25 @@ def test_refusals():
     assert (ttc.gemm_w4(x, q) == 0).all() and ttc.ff_device_status() == 0
 
 
+def test_codes_past_32_bits():
+    """An activation's code that no int holds is refused, not cut to one that exists."""
+    t = torch.float16
+    x, w = torch.zeros(4, 64, dtype=t, device="cuda"), torch.zeros(16, 64, dtype=t, device="cuda")
+    h, f = torch.zeros(4, 16, dtype=t, device="cuda"), torch.zeros(4, 16, device="cuda")
+    q = ttc.w4_pack(torch.zeros(16, 64, dtype=torch.uint8, device="cuda"),
+                    torch.ones(16, 1, dtype=t, device="cuda"), group=64)
+    m = ttc.mx_quantize(x, "mxfp8")
+    for act in (1 << 32, (1 << 32) + 3, -(1 << 32)):
+        for call in (lambda: ttc.gemm_gated(x, w, w, act), lambda: ttc.gemm_w4(x, q, act=act),
+                     lambda: ttc.gemm_gated_backward(h, x, w, w, f, f, act),
+                     lambda: ttc.gemm_gated_w4(x, q, q, act),
+                     lambda: ttc.gemm_mx(m, m, None, act)):
+            with pytest.raises(RuntimeError):
+                call()
+    with pytest.raises(OverflowError):
+        ttc.gemm_gated(x, w, w, 1 << 64)
+
+
 def test_gradients_are_not_lost_in_silence():
     """A backward pass through a result without a graph raises; calls without one are as before."""
     t = torch.float16

@@ -37,6 +37,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+// A code of an activation or a format: what no int holds is none, -1, which the libraries refuse.
+int code(PyObject* o) {
+  const int64_t v = integer(o);
+  return v == static_cast<int>(v) ? static_cast<int>(v) : -1;
+}
+
 // Code of the 16-bit type of a CUDA tensor.
 int dtype_of(const at::Tensor& t, const char* what) {
   const auto s = t.scalar_type();

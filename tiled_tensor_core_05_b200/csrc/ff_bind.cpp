@@ -80,7 +80,7 @@ PyObject* gated(PyObject* const* a, Py_ssize_t n) {
   const int64_t F = rows_of(wg, "w_gate");
   const Mat mg(wg, "w_gate", F, x.cols, x.type, x.device);
   const Mat mu(wu, "w_up", F, x.cols, x.type, x.device);
-  const int act = static_cast<int>(integer(a[3]));
+  const int act = code(a[3]);
   const bool save = a[5] == Py_True;
   // (with save the caller takes the gradients)
   const NoGraph no_graph(save ? Py_None : a[4],
@@ -118,7 +118,7 @@ PyObject* gated_backward(PyObject* const* a, Py_ssize_t n) {
   const Mat dh(tensor(a[0], "dh"), "dh", M, F, x.type, x.device);
   const Mat g(tensor(a[4], "gate"), "gate", M, F, at::kFloat, x.device);
   const Mat u(tensor(a[5], "up"), "up", M, F, at::kFloat, x.device);
-  const int act = static_cast<int>(integer(a[6]));
+  const int act = code(a[6]);
   Context c(x.device, a[9]);
   const at::Tensor dg = new_matrix(M, F, x.type, x.device), du = new_matrix(M, F, x.type, x.device);
   const Mat mdg(dg, "dg", M, F, x.type, x.device), mdu(du, "du", M, F, x.type, x.device);
@@ -167,7 +167,7 @@ PyObject* w4_gemm(PyObject* const* a, Py_ssize_t n) {
   const Input x(a[0], "x");
   const Weight w(a + 1, x);
   const int64_t N = integer(a[7]);
-  const int group = static_cast<int>(integer(a[8])), act = static_cast<int>(integer(a[10]));
+  const int group = code(a[8]), act = code(a[10]);
   const at::Tensor bias_t = a[9] == Py_None ? at::Tensor() : tensor(a[9], "bias");
   const void* bias =
       bias_t.defined() ? vector(bias_t, "bias", N, x.type, x.device) : nullptr;
@@ -190,7 +190,7 @@ PyObject* w4_gated(PyObject* const* a, Py_ssize_t n) {
   const Input x(a[0], "x");
   const Weight g(a + 1, x), u(a + 7, x);
   const int64_t F = integer(a[13]);
-  const int group = static_cast<int>(integer(a[14])), act = static_cast<int>(integer(a[15]));
+  const int group = code(a[14]), act = code(a[15]);
   const NoGraph no_graph(a[16], "gemm_gated_w4 has no backward pass", x.t);
   Context c(x.device, a[17]);
   const at::Tensor h =

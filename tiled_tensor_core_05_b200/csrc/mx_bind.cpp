@@ -42,7 +42,7 @@ struct MxOut {
 PyObject* quantize(PyObject* const* a, Py_ssize_t n) {
   expect(n, 6);
   const at::Tensor& x = tensor(a[0], "x");
-  const int dtype = dtype_of(x, "x"), format = static_cast<int>(integer(a[1]));
+  const int dtype = dtype_of(x, "x"), format = code(a[1]);
   if (x.dim() != 2) fail(PyExc_ValueError, "%s must be a matrix", "x");
   const int64_t rows = x.size(0), cols = x.size(1);
   const int64_t ldx = matrix(x, "x", rows, cols, x.scalar_type(), x.device());
@@ -61,7 +61,7 @@ PyObject* dequantize(PyObject* const* a, Py_ssize_t n) {
   expect(n, 9);
   const at::Tensor &data = tensor(a[0], "q.data"), &scales = tensor(a[1], "q.scales");
   const int64_t rows = integer(a[2]), cols = integer(a[3]), ld = integer(a[4]);
-  const int format = static_cast<int>(integer(a[5]));
+  const int format = code(a[5]);
   Context c(data.device(), a[8]);
   const at::Tensor out =
       a[6] != Py_None ? tensor(a[6], "out")
@@ -81,7 +81,7 @@ PyObject* dequantize(PyObject* const* a, Py_ssize_t n) {
 PyObject* rms_norm(PyObject* const* a, Py_ssize_t n) {
   expect(n, 10);
   const at::Tensor& x = tensor(a[0], "x");
-  const int dtype = dtype_of(x, "x"), format = static_cast<int>(integer(a[5]));
+  const int dtype = dtype_of(x, "x"), format = code(a[5]);
   const auto type = x.scalar_type();
   const at::Device device = x.device();
   if (x.dim() != 2) fail(PyExc_ValueError, "%s must be a matrix", "x");
@@ -135,7 +135,7 @@ PyObject* gemm(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor &bd = tensor(a[2], "b.data"), &bs = tensor(a[3], "b.scales");
   const int64_t M = integer(a[4]), N = integer(a[5]), K = integer(a[6]);
   const int64_t lda = integer(a[7]), ldb = integer(a[8]);
-  const int format = static_cast<int>(integer(a[9])), act = static_cast<int>(integer(a[11]));
+  const int format = code(a[9]), act = code(a[11]);
   const at::Device device = ad.device();
   Context c(device, a[14]);
   const at::Tensor out =
