@@ -26,6 +26,41 @@ def test_libraries_do_not_wait_for_the_binding(tmp_path, monkeypatch):
         ("libttcmx.so", "mx_*", sorted(s + ".o" for s in build.COMMON + build.MX_SOURCES))]
 
 
+@pytest.mark.parametrize("binding", [False, True])
+def test_every_library_is_linked(tmp_path, monkeypatch, binding):
+    """All three libraries, from the objects of their sources, with and without the binding; and an
+    error of the linker is not lost beside the binding's."""
+    linked, broken = {}, []
+
+    def link(lib, objs, exports, verbose):
+        linked[os.path.basename(lib)] = (exports, sorted(objs))
+        if os.path.basename(lib) in broken:
+            raise RuntimeError("link failed")
+
+    def bind(verbose):
+        if not binding:
+            raise RuntimeError("no g++")
+
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(build, "_compile", lambda src, info, verbose: src + ".o")
+    monkeypatch.setattr(build, "_link_library", link)
+    monkeypatch.setattr(build, "_build_bind", bind)
+    want = {name: (exports, sorted(s + ".o" for s in build.COMMON + sources)) for
+            name, exports, sources in (("libttc05.so", "gemm_*", build.SOURCES),
+                                       ("libttcmx.so", "mx_*", build.MX_SOURCES),
+                                       ("libttcff.so", "ff_*", build.FF_SOURCES))}
+    if binding:
+        assert build.build(force=True) == build.LIB
+    else:
+        with pytest.raises(RuntimeError, match="no g"):
+            build.build(force=True)
+    assert linked == want
+    for broken in [["libttcff.so"], ["libttc05.so"], ["libttcmx.so"]]:
+        with pytest.raises(RuntimeError) as e:
+            build.build(force=True)
+        assert "link failed" in (str(e.value), str(e.value.__cause__))
+
+
 def test_binding_of_another_torch_is_not_taken_for_current(tmp_path, monkeypatch):
     """The binding is compiled against one torch and one interpreter: with another version in use
     it is built again, and the old one is not loaded."""

@@ -53,8 +53,9 @@ def nvcc() -> str:
 
 
 def bind_path() -> str:
-    """The CPython bindings of libttcmx and libttcff, in one file, for the interpreter and the torch in use: its name holds
-    what it is compiled against, so that another version builds, and loads, one of its own."""
+    """The CPython bindings of libttcmx and libttcff, in one file, for the interpreter and the torch
+    in use: its name holds what it is compiled against, so that another version builds, and loads,
+    one of its own."""
     import sysconfig
 
     import torch
@@ -110,8 +111,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     # only the extern "C" API is exported: gemm_* of libttc05, mx_* of libttcmx, ff_* of libttcff
     _link(MX_LIB, [objs[s] for s in COMMON + MX_SOURCES], "mx_*", verbose)
     _link(LIB, [objs[s] for s in COMMON + SOURCES], "gemm_*", verbose)
-    bind.result()  # needs g++ and torch's headers, which the libraries do not
-    ff.result()
+    # the binding needs g++ and torch's headers, which the libraries do not; a library's error comes
+    # with the binding's, if both failed
+    errors = [e for e in (bind.exception(), ff.exception()) if e is not None]
+    if errors:
+        raise errors[0] from (errors[1] if errors[1:] else None)
     return LIB
 
 
@@ -131,8 +135,9 @@ def _build_bind(verbose: bool) -> None:
            "-I", sysconfig.get_paths()["include"], "-I", cuda]
     for d in cpp_extension.include_paths():
         cmd += ["-I", d]
-    cmd += [os.path.join(CSRC, f) for f in BIND_SOURCES] + ["-o", tmp, "-L", lib_dir, f"-Wl,-rpath,{lib_dir}",
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    cmd += [os.path.join(CSRC, f) for f in BIND_SOURCES]
+    cmd += ["-o", tmp, "-L", lib_dir, f"-Wl,-rpath,{lib_dir}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, capture_output=True, text=True)
