@@ -515,6 +515,126 @@ def test_w4_slices_of_rows():
         ref.close(ttc.gemm_w4(dev(x, t), part), *ref.w4_bound(x, w.value[a:b], None, "none", t))
 
 
+# ------------------------------------------------------- long sums, many tiles, few rows ---
+#
+# Sizes at which the kernels' rings of shared memory are gone through more than once (rings of
+# up to 7 places of 64 columns, 12 for the fewest rows; of up to 6 of 256 for 4 bits), K
+# divided and not, one wave of tiles and more.  References are 64-bit products on the GPU.
+
+SPLIT = [(250, 4096),   # F, D: few tiles, K in several parts of 8 blocks or more
+         (4700, 4096),  # 74 tiles
+         (6000, 1024),  # 94: one a CTA with the deep ring
+         (10300, 640)]  # 161: more than SMs
+
+
+@pytest.mark.parametrize("F,D", SPLIT)
+@pytest.mark.parametrize("M", [1, 4, 16, 30, 60, 100])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_long_sums(M, F, D, dtype):
+    t = DTYPES[dtype]
+    g = gen("long", M, F, D)
+    x, wg, wu = (integers(g, -1, 1, *s).cuda() for s in ((M, D), (F, D), (F, D)))
+    h, gate, up = ttc.gemm_gated(x.to(t), wg.to(t), wu.to(t), "relu", save=True)
+    a, b = x @ wg.t(), x @ wu.t()
+    assert torch.equal(gate.double(), a) and torch.equal(up.double(), b)
+    assert torch.equal(h, ref.rounded(a.clamp(min=0) * b, t))
+
+
+@pytest.mark.parametrize("F,D", [(2000, 256),    # two tiles, K in several parts
+                                 (520, 10000),   # 79: the deep ring
+                                 (264, 19200)])  # 150: more than SMs
+@pytest.mark.parametrize("M", [1, 4, 16, 30, 60, 100])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_backward_long_sums(M, F, D, dtype):
+    t = DTYPES[dtype]
+    backward_exact(t, gen("long backward", M, F, D), M, F, D)
+
+
+def backward_exact(t, g, M, F, D):
+    """Gradients of small integers, whose roundings to 16 bits and sums are exact."""
+    # gates and ups stay small: so many of x are 0 that a sum of D products, of which 4 in 9
+    # count otherwise, has a deviation of 3
+    x = integers(g, -1, 1, M, D) * (torch.rand((M, D), generator=g) < 9 / (D * 4 / 9))
+    x, wg, wu = (v.cuda() for v in (x, integers(g, -1, 1, F, D), integers(g, -1, 1, F, D)))
+    dh = integers(g, -2, 2, M, F).cuda()
+    r = ref.Gated(x, wg, wu, "relu")
+    want = r.backward(dh, t)
+    assert max(r.dg.abs().max(), r.du.abs().max()) <= 256
+    args = x.to(t), wg.to(t), wu.to(t)
+    _, gate, up = ttc.gemm_gated(*args, "relu", save=True)
+    got = ttc.gemm_gated_backward(dh.to(t), *args, gate, up, "relu")
+    for v, (k, (w, _)) in zip(got, want.items()):
+        assert torch.equal(v, ref.rounded(w, t)), k
+
+
+# dX on the kernel of large products: 48 tiles; 99, the second wave of which goes down K.  F is
+# no multiple of 64: the seam between the two pairs of operands lies inside a block.
+LARGE_DX = [(2000, 200, 1296), (2600, 136, 2104)]
+
+
+@pytest.mark.parametrize("M,F,D", LARGE_DX)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_backward_large_dx_exact(M, F, D, dtype):
+    t = DTYPES[dtype]
+    backward_exact(t, gen("large dx", M, F, D), M, F, D)
+
+
+@pytest.mark.parametrize("M,F,D", LARGE_DX + [(2000, 203, 1290), (2600, 139, 2101)])
+@pytest.mark.parametrize("name", ref.ACTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_backward_large_dx_random(M, F, D, name, dtype):
+    t = DTYPES[dtype]
+    g = gen("large dx", M, F, D, name, dtype)
+    x = normal(g, t, M, D, std=2.0).cuda()
+    wg, wu = (normal(g, t, F, D, std=2.0 / D ** 0.5).cuda() for _ in range(2))
+    dh = normal(g, t, M, F, std=0.3).cuda()
+    r = ref.Gated(x, wg, wu, name)
+    args = dev(x, t), dev(wg, t), dev(wu, t)
+    _, gate, up = ttc.gemm_gated(*args, name, save=True)
+    got = ttc.gemm_gated_backward(dev(dh, t), *args, gate, up, name)
+    for v, (k, (w, bound)) in zip(got, r.backward(dh, t).items()):
+        ref.close(v, w.cpu(), bound.cpu(), f"{k} {M} x {F} x {D} {name}")
+
+
+def w4_on_gpu(g, rows, cols, group, zeros, t):
+    """A weight with scales of powers of two, and its 64-bit values."""
+    groups = -(-cols // group)
+    codes = torch.randint(0, 16, (rows, cols), generator=g, dtype=torch.uint8).cuda()
+    scales = torch.exp2(torch.randint(-4, 0, (rows, groups), generator=g).double()).cuda()
+    z = torch.randint(0, 16, (rows, groups), generator=g, dtype=torch.uint8).cuda() if zeros else None
+    w = ttc.w4_pack(codes, scales.to(t), z, group=group)
+    at = torch.arange(cols, device="cuda") // group
+    value = codes.double() - (z.double()[:, at] if zeros else 8.0)
+    return w, value.mul_(scales[:, at])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 200, 16384), (4, 200, 32768), (8, 200, 16384),  # K > N
+                                   (13, 200, 16384), (30, 200, 16384), (61, 200, 16384),
+                                   (130, 200, 16384), (16, 70, 9000),
+                                   # one part; tiles for more than a wave
+                                   (16, 38000, 2600), (32, 38000, 2600), (64, 38000, 2600)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_w4_long_sums(M, N, K, group, dtype):
+    """Sums are exact: at most 32768 products of 7.5 in steps of a sixteenth, 22 bits."""
+    t = DTYPES[dtype]
+    g = gen("w4 long", M, N, K, group)
+    x = integers(g, -1, 1, M, K).cuda()
+    w, value = w4_on_gpu(g, N, K, group, group != 64, t)
+    want = x @ value.t()
+    assert torch.equal(ttc.gemm_w4(dev(x, t), w), ref.rounded(want, t))
+    # gated: the first and the last rows of the weight (a slice starts on 16 rows)
+    first, F = N // 2 // 16 * 16, N - N // 2 // 16 * 16
+
+    def part(a, b):
+        z = None if w.zeros is None else w.zeros[:, a:b]
+        return ttc.W4Tensor(w.data[a:b], w.scales[:, a:b], z, b - a, K, group)
+
+    got = ttc.gemm_gated_w4(dev(x, t), part(0, F), part(first, N), "relu")
+    gate, up = want[:, :F].float(), want[:, first:].float()
+    assert torch.equal(got, (gate.clamp(min=0) * up).to(t))
+
+
 # --------------------------------------------------------------- empty, use, refusals ---
 
 
