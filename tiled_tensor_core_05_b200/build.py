@@ -36,7 +36,6 @@ FF_SOURCES = ["ff_api.cu", "ff_pair.cu", "ff_split.cu", "ff_rows.cu", "ff_w4.cu"
               "ff_w4_few.cu"]
 HEADERS = ["sm100.cuh", "extent.h", "internal.h", "skinny_common.cuh", "tile_common.cuh",
            "mx_internal.h", "mx_common.cuh", "mx_umma.cuh", "ff_internal.h", "ff_common.cuh",
-           "ff_w4.cuh",
            "bind_common.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -104,7 +104,7 @@ at::Tensor new_matrix(int64_t rows, int64_t cols, at::ScalarType type, at::Devic
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 
 void expect(Py_ssize_t got, Py_ssize_t want) {
-  if (got != want) fail(PyExc_TypeError, "%s: wrong number of arguments", "mx");
+  if (got != want) fail(PyExc_TypeError, "%s takes %lld arguments", "the call", want);
 }
 
 template <class F>

@@ -36,16 +36,14 @@ __device__ __forceinline__ void value_and_slope(float x, float& value, float& sl
     value = x * p;
     slope = fmaf(value, 1.0f - p, p);
   } else if constexpr (ACT == kActGelu) {
-    constexpr float kU = 0.8493218002880191f;   // sqrt(1/2) sqrt(log2 e)
-    constexpr float kP = 0.31012659265624243f;  // 0.3725 / sqrt(log2 e)
-    const float u = fabsf(x) * kU;
-    const float t = rcp_approx(fmaf(u, kP, 1.0f));
-    float q = fmaf(-0.06968224048614502f, t, 0.20664797723293304f);
-    q = fmaf(q, t, -0.07991653680801392f);
-    q = fmaf(q, t, 0.15073831379413605f);
-    q = fmaf(q, t, 0.07959755510091782f);
-    q = fmaf(q, t, 0.10768866539001465f);
-    q = fmaf(q, t, 0.10492625832557678f);
+    const float u = fabsf(x) * mx::kGeluU;
+    const float t = rcp_approx(fmaf(u, mx::kGeluP, 1.0f));
+    float q = fmaf(mx::kGelu7, t, mx::kGelu6);
+    q = fmaf(q, t, mx::kGelu5);
+    q = fmaf(q, t, mx::kGelu4);
+    q = fmaf(q, t, mx::kGelu3);
+    q = fmaf(q, t, mx::kGelu2);
+    q = fmaf(q, t, mx::kGelu1);
     const float e = ex2_approx(-u * u);  // exp(-x^2 / 2)
     const float tail = q * t * e;
     const float phi = x < 0.0f ? tail : 1.0f - tail;

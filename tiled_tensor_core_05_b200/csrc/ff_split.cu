@@ -40,8 +40,6 @@ struct Cfg {
   static constexpr int kPartBytes = BN * kPartCols * 4;
   static constexpr int kSmemBytes = 1024 + kRing + (2 * kStages + 3) * 8 + 16;
   static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
-  // CTAs an SM holds at once (228 KiB of shared memory, 1 KiB of it per CTA the system's)
-  static constexpr int kPerSm = 228 * 1024 / (kSmemBytes + 1024);
   static_assert(kPartBytes + mx::slot_rows(BN, kMaxSplits) * kPartCols * 4 <= kRing, "parts");
   static_assert(kSmemBytes <= kMaxDynamicSmem, "shared memory budget");
 };
@@ -252,12 +250,12 @@ __global__ void __launch_bounds__(kThreads)
 // instead of 37.9 and 39.4; dX of 64 x 4096 <- 4096 2 us faster, of 8192 <- 8192 the same.)
 template <int BN, bool DEEP>
 int choose_splits(int64_t tiles, int64_t stages, const DeviceCtx& d) {
-  using C = Cfg<BN, DEEP>;
   static Residency residency[64];
   int splits = 1;
   for (int c = 2; c <= kMaxSplits && stages >= 4 * c; ++c) {
     const int n =
-        residency[d.device & 63].of(c, ff_split_kernel<BN, DEEP>, kThreads, C::kSmemBytes, d);
+        residency[d.device & 63].of(c, ff_split_kernel<BN, DEEP>, kThreads,
+                                    Cfg<BN, DEEP>::kSmemBytes, d);
     if (tiles <= n) splits = c;
   }
   return splits;

@@ -43,7 +43,7 @@
 // time, and everything waits at the end of each few.
 #include <atomic>
 
-#include "ff_w4.cuh"
+#include "ff_common.cuh"
 
 namespace ttc {
 namespace ff {

@@ -176,22 +176,30 @@ __device__ __forceinline__ void bulk_push(uint32_t dst, const void* src, uint32_
 // Seven terms and this form take as many instructions as five terms and a
 // selection of Phi(x) or 1 - Phi(-x): 8192 x 14336 x 4096 MXFP4 with bias 190.5 us
 // in both types, 192.5 with the form of sm100.cuh.
+constexpr float kGeluU = 0.8493218002880191f;   // sqrt(1/2) sqrt(log2 e)
+constexpr float kGeluP = 0.31012659265624243f;  // p / sqrt(log2 e)
+constexpr float kGelu1 = 0.10492625832557678f;
+constexpr float kGelu2 = 0.10768866539001465f;
+constexpr float kGelu3 = 0.07959755510091782f;
+constexpr float kGelu4 = 0.15073831379413605f;
+constexpr float kGelu5 = -0.07991653680801392f;
+constexpr float kGelu6 = 0.20664797723293304f;
+constexpr float kGelu7 = -0.06968224048614502f;
+
 __device__ __forceinline__ float2 gelu2_relative(float2 x) {
-  constexpr float kU = 0.8493218002880191f;   // sqrt(1/2) sqrt(log2 e)
-  constexpr float kP = 0.31012659265624243f;  // p / sqrt(log2 e)
   constexpr float kC = static_cast<float>(-0x1p-8 / 0.8493218002880191);
   float2 v;
   asm("min.NaN.f32 %0, %1, 0f71800000;" : "=f"(v.x) : "f"(x.x));
   asm("min.NaN.f32 %0, %1, 0f71800000;" : "=f"(v.y) : "f"(x.y));
-  const float2 u = __fmul2_rn(make_float2(fabsf(v.x), fabsf(v.y)), splat2(kU));
-  const float2 d = __ffma2_rn(u, splat2(kP), splat2(1.0f));
+  const float2 u = __fmul2_rn(make_float2(fabsf(v.x), fabsf(v.y)), splat2(kGeluU));
+  const float2 d = __ffma2_rn(u, splat2(kGeluP), splat2(1.0f));
   const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-  float2 q = __ffma2_rn(splat2(-0.06968224048614502f * kC), t, splat2(0.20664797723293304f * kC));
-  q = __ffma2_rn(q, t, splat2(-0.07991653680801392f * kC));
-  q = __ffma2_rn(q, t, splat2(0.15073831379413605f * kC));
-  q = __ffma2_rn(q, t, splat2(0.07959755510091782f * kC));
-  q = __ffma2_rn(q, t, splat2(0.10768866539001465f * kC));
-  q = __ffma2_rn(q, t, splat2(0.10492625832557678f * kC));
+  float2 q = __ffma2_rn(splat2(kGelu7 * kC), t, splat2(kGelu6 * kC));
+  q = __ffma2_rn(q, t, splat2(kGelu5 * kC));
+  q = __ffma2_rn(q, t, splat2(kGelu4 * kC));
+  q = __ffma2_rn(q, t, splat2(kGelu3 * kC));
+  q = __ffma2_rn(q, t, splat2(kGelu2 * kC));
+  q = __ffma2_rn(q, t, splat2(kGelu1 * kC));
   q = __fmul2_rn(q, t);
   const float2 w = __ffma2_rn(u, u, splat2(-8.0f));
   const float2 tail = __fmul2_rn(q, make_float2(ex2_approx(-w.x), ex2_approx(-w.y)));
