@@ -214,9 +214,11 @@ __device__ __forceinline__ void join_and_finish(const Tail& o, uint8_t* part, ui
   } else {
     __syncthreads();
   }
-  // (one answer a warp: a wait that runs out may have ended well for some of its lanes, and
-  // finish_rows exchanges sums between all of them)
-  const bool aborted = __any_sync(0xffffffffu, *abort_flag != 0);
+  // One answer a warp where finish_rows exchanges sums between its lanes: a wait that runs out
+  // may have ended well for some of them.  (Asked by all calls, the compiler makes a function of
+  // finish_rows: 1000 x 1000 -> 1000 15.1 us instead of 14.2.)
+  bool aborted = *abort_flag != 0;
+  if (splits > 1 && o.gated) aborted = __any_sync(0xffffffffu, aborted);
   if (splits > 1 && pull) {
     static_assert(kPullRows * 16 <= kThreads, "a row for 16 threads");
     float v[8] = {};
