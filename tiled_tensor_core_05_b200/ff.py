@@ -236,7 +236,7 @@ def _check_w4(w: W4Tensor, what: str, x: torch.Tensor) -> None:
         raise TypeError(f"{what} must be a W4Tensor")
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")
-    if x.dim() != 2 or x.shape[1] != w.cols:
+    if x.dim() != 2 or x.shape[1] != w._cols:
         raise ValueError(f"x must be a matrix of {w.cols} columns, got {tuple(x.shape)}")
 
 
@@ -248,7 +248,7 @@ def gemm_w4(x: torch.Tensor, w: W4Tensor, bias: torch.Tensor | None = None,
     points are exact and sums are fp32: no weight is rounded.  The weight is read once for every
     64 rows.  There is no backward pass: one that reaches y raises."""
     _check_w4(w, "w", x)
-    rc, y = (_bind or _loaded()).w4_gemm(x, *w._args, w.rows, w.group, bias, _act(act), out,
+    rc, y = (_bind or _loaded()).w4_gemm(x, *w._args, w._rows, w._group, bias, _act(act), out,
                                          _handle(stream))
     if rc:
         ops._check(rc, "ff_w4_gemm")
@@ -265,7 +265,7 @@ def gemm_gated_w4(x: torch.Tensor, w_gate: W4Tensor, w_up: W4Tensor, act: str | 
             (w_gate.zeros is None) != (w_up.zeros is None):
         raise ValueError(f"w_gate and w_up must share shape, group and zero points: {w_gate!r}, "
                          f"{w_up!r}")
-    rc, h = (_bind or _loaded()).w4_gated(x, *w_gate._args, *w_up._args, w_gate.rows, w_gate.group,
+    rc, h = (_bind or _loaded()).w4_gated(x, *w_gate._args, *w_up._args, w_gate._rows, w_gate._group,
                                           _act(act), out, _handle(stream))
     if rc:
         ops._check(rc, "ff_w4_gated")
