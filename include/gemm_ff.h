@@ -12,10 +12,11 @@
  * elements unless an entry point says otherwise and make rows start on 16 bytes
  * (a multiple of 8 elements of 16 bits, of 4 fp32 values, of 16 bytes).  Host
  * pointers and extents past the allocation are refused before any launch; calls
- * are asynchronous and stream-ordered; results are the same bits on every run;
- * errors found on the device are read with ff_get_device_status().  No entry point
- * throws, allocates device memory or keeps a reference to its arguments, so calls
- * on several streams or host threads share nothing, and every call can be captured
+ * are asynchronous and stream-ordered; results are the same bits on every run on one
+ * GPU (into how many parts a sum is divided depends on the sizes and on how many
+ * clusters the GPU holds); errors found on the device are read with
+ * ff_get_device_status().  No entry point throws, allocates device memory or keeps a
+ * reference to its arguments, so calls on several streams or host threads share nothing, and every call can be captured
  * in a CUDA graph (make one such call outside a capture first: it looks up the
  * device and sets up the kernels).  Outputs must not overlap inputs or each other.
  *
@@ -37,7 +38,7 @@ enum ff_activation { FF_ACT_SILU = 3 };
  *   X: M x D, Wg, Wu: F x D, H: M x F, of type `dtype` (MX_F16 or MX_BF16);
  *   G, U: M x F fp32, the two projections before the activation, for
  *         ff_gated_backward; both or neither (NULL).
- * Sums and everything up to H's one rounding are fp32.  Sizes in [0, 2^31 - 1];
+ * Sums and everything up to H's one rounding are fp32.  Sizes in [0, 2^31 - 256];
  * without rows or without columns F a no-op; D == 0 gives zeros. */
 GEMM_API int ff_gated(const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                       int64_t M, int64_t F, int64_t D, int64_t ldx, int64_t ldwg, int64_t ldwu,
@@ -49,8 +50,9 @@ GEMM_API int ff_gated(const void* X, const void* Wg, const void* Wu, void* H, vo
  *   dX  = dG Wg + dU Wu                   (NULL: not computed)
  *   dWg = dG^T X,  dWu = dU^T X           (both or neither NULL)
  * dG and dU (M x F, type dtype) are written by every call: each is rounded once, for
- * the tensor cores; everything before is fp32, as are the sums.  act'(0) is 0 for
- * ReLU.  With F == 0 dX is zeros, with M == 0 dWg and dWu are. */
+ * the tensor cores; everything before is fp32, as are the sums.  (In fp16 a dG or dU of
+ * more than 65504 in magnitude is infinite there and one below 2^-25 zero: scale dH, as
+ * is usual with fp16 gradients, or take bf16.)  act'(0) is 0 for ReLU.  With F == 0 dX is zeros, with M == 0 dWg and dWu are. */
 GEMM_API int ff_gated_backward(const void* dH, const void* X, const void* Wg, const void* Wu,
                                const void* G, const void* U, void* dG, void* dU, void* dX,
                                void* dWg, void* dWu, int64_t M, int64_t F, int64_t D,
@@ -73,8 +75,9 @@ GEMM_API int ff_gated_backward(const void* dH, const void* X, const void* Wg, co
  * Y = act(X W^T + bias).  X: M x K, Y: M x N, bias: N values or NULL, of type dtype.
  * Codes and zero points are exact, the sums of a group are fp32 and take its scale
  * there: no weight is rounded.  (With up to 8 rows a group's codes and its zero point
- * are summed apart, so that an fp32 sum's error counts code + zero, not their difference.)  Made for few rows: a weight is read once for
- * every 64 of them.  K == 0 gives act(bias). */
+ * are summed apart, so that an fp32 sum's error counts code + zero, not their
+ * difference, and x is held to 2^-35 of the largest value of its row in the group.)  Made
+ * for few rows: a weight is read once for every 64 of them.  K == 0 gives act(bias). */
 GEMM_API int ff_w4_gemm(const void* X, const void* Q, const void* S, const void* Z,
                         const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int64_t ldx,
                         int64_t ldq, int64_t lds, int64_t ldz, int64_t ldy, int group, int dtype,

@@ -51,8 +51,16 @@ int fill_zeros(void* p, int64_t rows, int64_t cols, int64_t ld, cudaStream_t str
   return e == cudaSuccess ? GEMM_OK : runtime_error();
 }
 
-// Whether the pair kernel takes a product of M rows in tiles of 256 x `cols`: where its
-// tiles fill a quarter of the SMs.
+// The pair kernel takes a product of more than 64 rows whose tiles of 256 x `cols` are at least
+// a quarter as many as the SMs (each tile takes two), and all weight gradients.  Measured, pair
+// and split kernel:
+//   gated    128 tiles (1000 x 4096 -> 4096) 48.7 and 92.7 us, 112 (96 x 4096 -> 14336) 51.1 and
+//            52.1, 64 (512 x 1024 -> 4096) 10.9 and 23.8; 32 tiles: 24.6 and 25.0 (256 x 4096 ->
+//            4096), 9.8 and 11.9 (1000 x 1024 -> 1000), but 24.1 and 16.5 (96 x 4096 -> 4096);
+//            16 (512 x 1024 -> 1000) 9.4 and 9.2, 8 (128 x 1024 -> 1000) 9.3 and 7.3
+//   dX       64 tiles (1000 x 4096 <- 14336) 193.7 and 267.3, 32 (512 x 4096 <- 4096) 48.2 and
+//            45.2, 16 (1000 x 1024 <- 4096) 50.7 and 33.7
+//   64 rows  112 tiles (64 x 4096 -> 14336, gated) 50.4 and 40.7
 int run_product(const Product& p, const DeviceCtx& d) {
   const int64_t cols = p.form == kGated ? 128 : 256;
   const int64_t pair_tiles = (p.M + 255) / 256 * ((p.N + cols - 1) / cols);

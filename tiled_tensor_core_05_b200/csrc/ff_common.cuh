@@ -75,8 +75,8 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 // A kernel that divides K leaves each CTA of a cluster with a part of the tile's
 // fp32 sums: rows of kPartCols values in its shared memory.  CTA r finishes the rows
 // [rows r / n, rows (r + 1) / n): the others send it theirs (one bulk copy between
-// the SMs' shared memories each) and it adds the parts in rank order, which depends
-// on the shape alone.  Up to kPullRows rows the first CTA reads the others' parts
+// the SMs' shared memories each) and it adds the parts in rank order; their number
+// depends on the shape and on how many clusters the GPU holds.  Up to kPullRows rows the first CTA reads the others' parts
 // instead: copies would take longer than the loads.
 constexpr int kPartCols = 128;
 constexpr int kMaxSplits = 8;  // CTAs of a cluster

@@ -8,7 +8,8 @@
 // weights MN-major as they are stored (F x D), the k-blocks of the second pair of
 // operands after those of the first.  The K range of a tile is divided among the
 // CTAs of a cluster, whose parts are joined in shared memory (ff_common.cuh):
-// nothing is kept in device memory, and the order of the sums is fixed by the shape.
+// nothing is kept in device memory, and the order of the sums is fixed by the shape and the
+// number of parts, which is the same for every call of a shape on one GPU.
 //
 //   warp 0     TMA producer into a ring of 128-byte-swizzled stages
 //   warp 1     TMEM, tcgen05.mma
@@ -327,7 +328,11 @@ int launch(const Product& p, const DeviceCtx& d) {
 }
 
 // Where the tiles alone give most SMs one CTA, one with a deep ring and the whole of
-// K; else two an SM, which also cover each other's ends.
+// K; else two an SM, which also cover each other's ends.  Measured, one with a deep ring and
+// two, gated, D = 4096, 1 and 64 rows: F = 6000 (94 tiles) 19.5 and 22.4 us, 20.5 and 26.3;
+// 8000 (125) 24.6 and 24.7, 25.2 and 28.2; 14336 (224) 44.2 and 48.9, 39.6 and 40.7.  With K in
+// parts the deep ring is ahead, too, by less (2000, 32 tiles: 9.4 and 10.7, 9.7 and 12.1; 4000,
+// 63: 13.9 and 14.9, 13.9 and 16.9): not taken.
 template <int BN>
 int launch_tile(const Product& p, const DeviceCtx& d) {
   const int cols = p.form == kGated ? 64 : kPartCols;
@@ -338,6 +343,9 @@ int launch_tile(const Product& p, const DeviceCtx& d) {
 
 }  // namespace
 
+// Tiles of 128 rows from 65 on (an SM holds one such CTA: a stage takes 32 KB).  Against 64
+// rows: gated, D = 4096 -> F = 4096, 96 rows 16.5 us and 21.5, 256 rows 25.0 and 26.6; dX of 96 x
+// 4096 <- 14336 42.7 and 73.8; of 96 x 1024 <- 1000 8.3 and 8.1.
 int launch_split_product(const Product& p, const DeviceCtx& d) {
   if (p.M <= 16) return launch_tile<16>(p, d);
   if (p.M <= 32) return launch_tile<32>(p, d);

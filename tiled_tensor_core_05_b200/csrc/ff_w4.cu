@@ -16,6 +16,10 @@
 //              group has sums of its own, so that no weight is rounded
 //   warp 8     TMA producer
 //   warp 9     tcgen05.mma, A from TMEM (two buffers), B (x) from shared memory
+//
+// Bound by warps 0-7: 16 x 28672 x 8192 takes 52.9 us, 31 instructions for a word of 8 codes,
+// which an SM with two tiles issues at 77 % of its slots (ALU 74 %), 21 codes a clock; the SMs
+// with one tile (72 of 148: 224 tiles) are half as busy.  DRAM 26 %.
 #include <atomic>
 
 #include "ff_common.cuh"

@@ -34,9 +34,10 @@
 //
 // Measured (calls in turn on weights from memory), 128 columns a group: 1 x 14336 x 4096
 // 12.1 us (2.5 TB/s), gated 19.5 us (3.1 TB/s), 1 x 28672 x 8192 28.4 us (4.3 TB/s), 8 rows
-// 45 us.  The fixed part is 4 us (5 x 1000 x 1000).  The largest products are bound by issue:
-// with the weights brought by cp.async, whose addresses and edges cost as many instructions
-// as the products, they took 16.5, 26.2 and 43.1 us.  12 warps: 12.5, 21.5, 31.1 us; 20:
+// 45 us.  The fixed part is 4 us (5 x 1000 x 1000).  In the largest products issue slots and
+// memory are each half busy: what is left are the chains of masks and MMAs of four warps a
+// scheduler.  With the weights brought by cp.async, whose addresses and edges cost as many
+// instructions as the products, they took 16.5, 26.2 and 43.1 us.  12 warps: 12.5, 21.5, 31.1 us; 20:
 // 12.6, 20.4, 28.0; 24: 13.7, 21.3, 29.1; 3 blocks on their way instead of 2: 12.2, 20.3,
 // 28.9, and fewer rows fit.  16 rows with K divided among a cluster of 4, so that x fits,
 // took 125 us, the kernel of more rows 53: sums of 16 warps and rows hold few tiles at a
