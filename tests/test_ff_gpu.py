@@ -873,12 +873,15 @@ def test_gradients_are_not_lost_in_silence():
     def leaf(v):
         return v.detach().requires_grad_()
 
+    learned = ttc.W4Tensor(w.data, leaf(w.scales), None, 16, 64, 64)  # (its scales)
     calls = [(h, lambda **k: ttc.gemm_gated(leaf(x), wg, wu, **k), "gemm_gated_backward"),
              (h, lambda **k: ttc.gemm_gated(x, leaf(wg), wu, **k), "gemm_gated_backward"),
              (h, lambda **k: ttc.gemm_gated(x, wg, leaf(wu), **k), "gemm_gated_backward"),
              (y, lambda **k: ttc.gemm_w4(leaf(x), w, b, **k), "gemm_w4 has no"),
              (y, lambda **k: ttc.gemm_w4(x, w, leaf(b), **k), "gemm_w4 has no"),
-             (z, lambda **k: ttc.gemm_gated_w4(leaf(x), w, w, **k), "gemm_gated_w4 has no")]
+             (y, lambda **k: ttc.gemm_w4(x, learned, b, **k), "gemm_w4 has no"),
+             (z, lambda **k: ttc.gemm_gated_w4(leaf(x), w, w, **k), "gemm_gated_w4 has no"),
+             (z, lambda **k: ttc.gemm_gated_w4(x, w, learned, **k), "gemm_gated_w4 has no")]
     for want, call, message in calls:
         got = call()
         assert torch.equal(got.detach(), want) and got.requires_grad
@@ -891,6 +894,12 @@ def test_gradients_are_not_lost_in_silence():
         with torch.no_grad():
             assert call(out=out) is out and torch.equal(out, want)
             assert not call().requires_grad
+    # nor is it handed out as None, and a kept result holds nothing of the inputs' gradients
+    v = leaf(x)
+    got = ttc.gemm_gated(v, wg, wu)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(got.float().sum(), v)
+    assert got.grad_fn.next_functions == ()
     # with save the gradients are the caller's own business
     results = ttc.gemm_gated(leaf(x), leaf(wg), leaf(wu), save=True)
     assert torch.equal(results[0], h) and not any(v.requires_grad for v in results)

@@ -51,6 +51,8 @@ struct Input {  // a matrix of activations and what follows from it
 
 // These operators record no graph.  Where an input requires a gradient, a backward pass that
 // reaches their result raises `message`: without it the gradient would be lost in silence.
+// (The node has no edges to the inputs: a result that is kept would keep their gradients'
+// accumulators, and with them the stream of this call, for a backward pass captured later.)
 // As with torch's own out= forms, a given result (`out`) is refused then, before anything runs.
 struct NoGraph {
   std::shared_ptr<torch::autograd::Node> node;
@@ -59,8 +61,7 @@ struct NoGraph {
     if (!torch::autograd::compute_requires_grad(inputs...)) return;
     if (out != Py_None)
       fail(PyExc_RuntimeError, "out= is for inputs that require no gradient: %s", message);
-    node = std::make_shared<torch::autograd::Error>(
-        message, torch::autograd::collect_next_edges(inputs...));
+    node = std::make_shared<torch::autograd::Error>(message);
   }
   void mark(const at::Tensor& result) const {
     if (node) torch::autograd::set_history(result, node);
@@ -146,9 +147,9 @@ PyObject* gated_backward(PyObject* const* a, Py_ssize_t n) {
 struct Weight {
   const void *q, *s, *z = nullptr;
   int64_t ldq, lds, ldz = 0;
-  static constexpr int kArgs = 6;
-  Weight(PyObject* const* a, const Input& x) {
-    const at::Tensor &data = tensor(a[0], "w.data"), &scales = tensor(a[1], "w.scales");
+  const at::Tensor& scales;
+  Weight(PyObject* const* a, const Input& x) : scales(tensor(a[1], "w.scales")) {
+    const at::Tensor& data = tensor(a[0], "w.data");
     if (data.device() != x.device) fail(PyExc_ValueError, "%s is on another device", "w");
     if (scales.scalar_type() != x.type)
       fail(PyExc_TypeError, "%s have another type than x", "the scales of w");
@@ -171,7 +172,7 @@ PyObject* w4_gemm(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor bias_t = a[9] == Py_None ? at::Tensor() : tensor(a[9], "bias");
   const void* bias =
       bias_t.defined() ? vector(bias_t, "bias", N, x.type, x.device) : nullptr;
-  const NoGraph no_graph(a[11], "gemm_w4 has no backward pass", x.t, bias_t);
+  const NoGraph no_graph(a[11], "gemm_w4 has no backward pass", x.t, bias_t, w.scales);
   Context c(x.device, a[12]);
   const at::Tensor y =
       a[11] != Py_None ? tensor(a[11], "out") : new_matrix(x.rows, N, x.type, x.device);
@@ -191,7 +192,8 @@ PyObject* w4_gated(PyObject* const* a, Py_ssize_t n) {
   const Weight g(a + 1, x), u(a + 7, x);
   const int64_t F = integer(a[13]);
   const int group = code(a[14]), act = code(a[15]);
-  const NoGraph no_graph(a[16], "gemm_gated_w4 has no backward pass", x.t);
+  const NoGraph no_graph(a[16], "gemm_gated_w4 has no backward pass", x.t, g.scales,
+                         u.scales);
   Context c(x.device, a[17]);
   const at::Tensor h =
       a[16] != Py_None ? tensor(a[16], "out") : new_matrix(x.rows, F, x.type, x.device);
