@@ -480,15 +480,15 @@ def test_w4_large_bf16_values(M, group, zeros):
     x = normal(g, t, M, K)
     w = W4(g, N, K, group, zeros, t)
     base = ttc.gemm_w4(dev(x, t), w.w).cpu()
-    for exponent in (117, 118, 119, 122):
+    for exponent in (115, 116, 119, 122):
         x[M - 1, 133] = 2.0 ** exponent
         want, r = x @ w.value.t(), ref.HALF[t]
         assert want.abs().max() < 2.0 ** 127
         got = ttc.gemm_w4(dev(x, t), w.w).cpu()
         assert torch.equal(got[:M - 1], base[:M - 1])
-        # summed in one chain of fp32 additions a group, then one of the groups (from 2^118 on; below,
+        # summed in one chain of fp32 additions a group, then one of the groups (from 2^116 on; below,
         # codes and zero points apart, to which a code at its zero point is no exception)
-        if exponent >= 118:
+        if exponent >= 116:
             off = (group + -(-K // group)) * 2.0 ** -24 * (x.abs() @ w.value.abs().t())
         else:
             both = ref.weight(w.codes, w.scales.abs(), -w.zeros if zeros else
@@ -501,7 +501,26 @@ def test_w4_large_bf16_values(M, group, zeros):
         ref.close(got[M - 1:], want[M - 1:],
                   (off * (1 + r) + r * want.abs() + ref.TINY[t])[M - 1:], f"2^{exponent}")
     # (a column whose code is its zero point was among them)
-    assert exponent >= 118 and (want[M - 1].abs() < 2.0 ** 20).any()
+    assert exponent >= 116 and (want[M - 1].abs() < 2.0 ** 20).any()
+
+
+@pytest.mark.parametrize("M", [1, 8])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_large_bf16_sums(M, group):
+    """Sums of a group that pass bf16's and fp32's largest value, and results that do not."""
+    t = torch.bfloat16
+    N, K = 40, 256
+    codes = torch.full((N, K), 15, dtype=torch.uint8, device="cuda")
+    scales = torch.full((N, K // group), 2.0 ** -12, dtype=t, device="cuda")
+    for zero, factor in ((0, 15 / 16), (7, 1 / 2), (None, 7 / 16)):
+        zeros = None if zero is None else torch.full((N, K // group), zero, dtype=torch.uint8,
+                                                     device="cuda")
+        w = ttc.w4_pack(codes, scales, zeros, group=group)
+        for exponent in (114, 115, 116, 117, 120, 126, 127):
+            for mantissa in (1.0, 1.25, 1.9921875):
+                x = torch.full((M, K), mantissa * 2.0 ** exponent, dtype=t, device="cuda")
+                want = torch.tensor(mantissa * 2.0 ** exponent * factor).to(t)
+                assert (ttc.gemm_w4(x, w).cpu() == want).all(), (zero, exponent, mantissa)
 
 
 def test_w4_slices_of_rows():

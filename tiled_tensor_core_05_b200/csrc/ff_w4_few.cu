@@ -14,8 +14,8 @@
 //     sum (code - zero) x = e (sum (code 2^-24) y - zero sum 2^-24 y),
 // and the group's scale is applied to that: no weight is rounded.  (The scale comes last, so
 // that fp32 holds the group's sum itself, not a part of 2^24 of it: bf16 results keep their bits
-// down to bf16's smallest.)  Rows of x with infinities or with values of 2^118 and more, whose e
-// fp32 cannot hold, are summed plainly.
+// down to bf16's smallest.)  Rows of x with infinities or with values of 2^116 and more, whose
+// sums fp32 may not hold, are summed plainly.
 //
 // A CTA an SM goes through its tiles of 16 rows of the weights (gated: 8 of each); its
 // warps take the tiles' blocks of 256 columns in turn, each with its own ring in shared
@@ -102,8 +102,9 @@ __device__ __forceinline__ void mma16816(float2 (&d)[2], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The bits of 2^118: from there on a row is summed plainly.
-constexpr uint32_t kPlainFrom = (127u + 118u) << 23;
+// The bits of 2^116: from there on a row is summed plainly.  (A group's sum, of up to 128
+// products with 15, stays below 2^11 times 2^116.)
+constexpr uint32_t kPlainFrom = (127u + 116u) << 23;
 
 // y, e and the sums of y of a row's block, 8 columns a lane.  bits: of the group's largest
 // magnitude; a NaN's or an infinity's is above all others.
@@ -140,7 +141,7 @@ __device__ __forceinline__ uint4 prepare8(const uint4& raw, uint32_t& bits, floa
 }
 
 // The sum of a row of x times a row of a weight, for rows that the split into e and y cannot
-// hold.
+// hold.  x counts 2^-16, so that a group's sum is in range wherever the result is.
 template <class T, int GROUP>
 __device__ __noinline__ float plain_sum(const uint16_t* x, const W4Weight& w, int n, int K) {
   const uint8_t* q = static_cast<const uint8_t*>(w.Q) + n * w.ldq;
@@ -154,11 +155,11 @@ __device__ __noinline__ float plain_sum(const uint16_t* x, const W4Weight& w, in
       // column 2 i of a word's 8 in bits 4 i, column 2 i + 1 in bits 4 i + 16
       const int byte = (k >> 3) * 4 + (k & 1) * 2 + ((k >> 2) & 1);
       const int code = (q[byte] >> ((k & 2) * 2)) & 15;
-      sum = fmaf(static_cast<float>(code) - zero, mx::unpack2<T>(x[k]).x, sum);
+      sum = fmaf(static_cast<float>(code) - zero, 0x1p-16f * mx::unpack2<T>(x[k]).x, sum);
     }
     total = fmaf(sum, mx::unpack2<T>(static_cast<const uint16_t*>(w.S)[i * w.lds + n]).x, total);
   }
-  return total;
+  return 0x1p16f * total;
 }
 
 template <class T, int GROUP, bool GATED>
